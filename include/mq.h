@@ -367,6 +367,106 @@ MQ_API mq_status mq_unpack(const mq_weights *w, uint8_t *codes_out, void *stream
 MQ_API mq_status mq_gemv_noalloc(const uint16_t *X_dev, const mq_weights *w, int64_t M,
                                  int64_t N, int64_t K, uint16_t *Y_dev, void *stream);
 
+/* ---------------------------------------------------------------------------
+ * MXFP4: microscaled 4-bit floating point, the format this GPU's tensor cores
+ * multiply at four times the bf16 rate.  Every 32 consecutive columns of a row
+ * share a power-of-two scale; an element is a 4-bit float (e2m1).
+ *
+ * Definition, for a block of 32 values with a = max |v|:
+ *   e    = max(floor(log2 a) - 2, -127);  scale byte E = e + 127 (0 when a = 0)
+ *   c    = |v| 2^-e rounded to {0, 0.5, 1, 1.5, 2, 3, 4, 6}, to nearest, ties
+ *          to the even code; above 6 gives 6 (a 2^-e lies below 8)
+ *   code = index of c, plus 8 when the sign bit of v is set
+ *   the element stands for +-c 2^(E - 127)
+ * A block that holds a NaN or an infinity gets E = 255 and zero codes: all of
+ * it stands for NaN, and so does every output its row or feature enters.
+ *
+ * Storage of a rows x K matrix, K a positive multiple of 32:
+ *   codes   rows x K/2 bytes, row-major: byte j of a row holds column 2j in
+ *           its low four bits and column 2j + 1 in its high four
+ *   scales  blocks of 512 bytes, one per 128 rows x 128 columns (partial ones
+ *           whole), the blocks of a row band one after another; inside a
+ *           block the byte of row i (0..127) and column group j (0..3, of 32)
+ *           is at (i % 32) * 16 + (i / 32) * 4 + j.  Bytes of rows and
+ *           columns beyond the matrix are 0.
+ * Both buffers 16-byte aligned.
+ */
+typedef struct mq_mx4 {
+    const uint8_t *codes;    /* device: mq_mx4_code_bytes(rows, K) bytes */
+    const uint8_t *scales;   /* device: mq_mx4_scale_bytes(rows, K) bytes */
+    int64_t rows;            /* rows (tokens, or output features) */
+    int64_t K;               /* columns, a positive multiple of 32 */
+} mq_mx4;
+
+/* Types of dense values beside MXFP4 matrices. */
+enum {
+    MQ_BF16 = 0,
+    MQ_F16 = 1,
+    MQ_F32 = 2
+};
+
+/* Bytes of the two buffers (0 on invalid sizes: rows < 0 or > 2^31 - 256, K
+ * not a positive multiple of 32 or > 2^31 - 256; 0 also for rows = 0). */
+MQ_API size_t mq_mx4_code_bytes(int64_t rows, int64_t K);
+MQ_API size_t mq_mx4_scale_bytes(int64_t rows, int64_t K);
+
+/*
+ * Dense rows -> MXFP4: activations each step, float weights once.
+ *   X_dev       rows x K values of type dtype (MQ_BF16, MQ_F16, MQ_F32), row i
+ *               at element i * ld
+ *   codes_out, scales_out  the two buffers (all of their bytes are written)
+ * Preconditions: the sizes above, ld >= K, X and the bytes of a row's stride
+ * multiples of 16, the outputs 16-byte aligned and not overlapping X.
+ * rows == 0 does nothing.
+ */
+MQ_API mq_status mq_mx4_quantize(const void *X_dev, int dtype, int64_t rows, int64_t K, int64_t ld,
+                                 uint8_t *codes_out, uint8_t *scales_out, void *stream);
+
+/*
+ * The r-bit model of a nested parent -> MXFP4 (w->N x w->K): the weights
+ * s (2^(8-r) q_r + 2^(7-r) - z), z = 128 without zero points, taken exactly (no
+ * intermediate rounding) and rounded once to the format above.  Reads the
+ * first r planes, so a nested checkpoint serves the 4-bit products without a
+ * dense copy.  Preconditions on w as mq_gemm; the outputs as mq_mx4_quantize.
+ */
+MQ_API mq_status mq_mx4_from_nested(const mq_weights *w, uint8_t *codes_out, uint8_t *scales_out,
+                                    void *stream);
+
+/*
+ * The values an MXFP4 matrix stands for: out (rows x K of type dtype, MQ_BF16
+ * or MQ_F32, row i at element i * ld; both types hold every value exactly).
+ * Preconditions: ld >= K, out and the bytes of a row's stride multiples of 16.
+ */
+MQ_API mq_status mq_mx4_dequantize(const mq_mx4 *m, void *out_dev, int dtype, int64_t ld, void *stream);
+
+/*
+ * Y = X . W^T of two MXFP4 matrices (X: M x K activations, w: N x K weights),
+ * fp32 sums in a fixed order (results are deterministic), rounded once to
+ * y_dtype (MQ_BF16, MQ_F16, MQ_F32).  Y is M x N, row i at element i * ldy.
+ * Preconditions: equal K, ldy >= N, every pointer 16-byte aligned, Y not
+ * overlapping the inputs.  M == 0 does nothing; nothing beyond the N columns of
+ * a row is written.
+ */
+MQ_API mq_status mq_mx4_gemm(const mq_mx4 *X, const mq_mx4 *w, void *Y_dev, int y_dtype, int64_t ldy,
+                             void *stream);
+
+/*
+ * Y = X . W^T with bf16 activations kept (weights only in 4 bits): single
+ * tokens and small batches.  X is M x w->K bf16, row i at element i * ldx.  A
+ * row of X is written as a sum of eight MXFP4 rows (within 2^-22 of the largest
+ * value of each block of 32), which meet the weights on the 4-bit tensor
+ * cores.
+ *   workspace  device buffer of mq_mx4_gemm_bf16_workspace_bytes(M, N, K)
+ *              bytes, contents arbitrary before and after (may be NULL when
+ *              that is 0).  Calls that can overlap must not share it.
+ * Preconditions as mq_mx4_gemm, and ldx >= K with a row's stride a multiple of
+ * 16 bytes.
+ */
+MQ_API size_t mq_mx4_gemm_bf16_workspace_bytes(int64_t M, int64_t N, int64_t K);
+MQ_API mq_status mq_mx4_gemm_bf16(const uint16_t *X_dev, int64_t M, int64_t ldx, const mq_mx4 *w,
+                                  void *Y_dev, int y_dtype, int64_t ldy, void *workspace,
+                                  size_t workspace_bytes, void *stream);
+
 /* Status of the most recent failing call on this host thread (MQ_OK if none). */
 MQ_API mq_status mq_last_error(void);
 

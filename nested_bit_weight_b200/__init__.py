@@ -19,6 +19,8 @@ __all__ = [
     "mq_set_gemv_variant", "mq_get_gemv_variant", "GEMV_TC", "GEMV_VIA_GEMM",
     "mq_device_status", "mq_gemm_kernel", "uses_gemv", "KERNEL_GEMV", "KERNEL_GEMM",
     "MqCall", "mq_gemm_chain", "gemm_chain", "pack_fused", "workspace_for", "mq_pack_zeros",
+    "MqMx4", "Mx4Matrix", "mx4_quantize", "mx4_from_nested", "mx4_dequantize", "mx4_gemm", "mx4_gemm_bf16",
+    "mq_mx4_code_bytes", "mq_mx4_scale_bytes", "mq_mx4_gemm_bf16_workspace_bytes",
     "MqChoice", "bitwidth_search", "layer_errors", "matgptq_prepare", "matgptq_quantize",
 ]
 
@@ -45,6 +47,12 @@ class MqWeights(ctypes.Structure):
                 ("zeros", ctypes.c_void_p)]                # fp16 zero points or None (symmetric)
 
 
+class MqMx4(ctypes.Structure):
+    """Mirror of the C struct mq_mx4 (an MXFP4 matrix, owns nothing)."""
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p),
+                ("rows", ctypes.c_int64), ("K", ctypes.c_int64)]
+
+
 class MqChoice(ctypes.Structure):
     """One candidate of mq_bitwidth_search (mq_choice in include/mq.h)."""
     _fields_ = [("r", ctypes.c_int32), ("bytes", ctypes.c_uint64), ("error", ctypes.c_double)]
@@ -63,7 +71,7 @@ def _load() -> ctypes.CDLL:
             "`python nested_bit_weight_b200/_build.py` (nvcc, sm_100a)")
     L = ctypes.CDLL(library_path)
     P, I64, I, SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t
-    W = ctypes.POINTER(MqWeights)
+    W, X4 = ctypes.POINTER(MqWeights), ctypes.POINTER(MqMx4)
     sig = {
         "mq_plane_bytes": (SZ, [I64, I64, I]),
         "mq_scale_bytes": (SZ, [I64, I64, I]),
@@ -82,6 +90,14 @@ def _load() -> ctypes.CDLL:
         "mq_gemm_kernel": (I, [I64, I64, I64, I]),
         "mq_gemm_chain": (I, [ctypes.POINTER(MqCall), I, P, SZ, P]),
         "mq_pack_zeros": (I, [P, I64, I64, I, P, P]),
+        "mq_mx4_code_bytes": (SZ, [I64, I64]),
+        "mq_mx4_scale_bytes": (SZ, [I64, I64]),
+        "mq_mx4_quantize": (I, [P, I, I64, I64, I64, P, P, P]),
+        "mq_mx4_from_nested": (I, [W, P, P, P]),
+        "mq_mx4_dequantize": (I, [X4, P, I, I64, P]),
+        "mq_mx4_gemm": (I, [X4, X4, P, I, I64, P]),
+        "mq_mx4_gemm_bf16_workspace_bytes": (SZ, [I64, I64, I64]),
+        "mq_mx4_gemm_bf16": (I, [P, I64, I64, X4, P, I, I64, P, SZ, P]),
         "mq_bitwidth_search": (I, [ctypes.POINTER(MqChoice), I, I, ctypes.c_uint64,
                                    ctypes.POINTER(I), ctypes.POINTER(ctypes.c_double)]),
         "mq_matgptq_prepare": (I, [P, I64, ctypes.c_double, P]),
@@ -365,4 +381,250 @@ def gemm(X, weights: NestedWeights, r: int, Y=None, stream=None):
     need = mq_gemm_workspace_bytes(M, weights.N, K, r)
     ws = workspace_for(X.device, need) if need else None
     mq_gemm(X, w, Y, ws, stream)
+    return Y
+
+
+# ----------------------------------------------- MXFP4 (microscaled 4-bit floats)
+
+BF16, F16, F32 = 0, 1, 2
+
+
+def mq_mx4_code_bytes(rows: int, K: int) -> int:
+    return lib.mq_mx4_code_bytes(rows, K)
+
+
+def mq_mx4_scale_bytes(rows: int, K: int) -> int:
+    return lib.mq_mx4_scale_bytes(rows, K)
+
+
+def mq_mx4_gemm_bf16_workspace_bytes(M: int, N: int, K: int) -> int:
+    return lib.mq_mx4_gemm_bf16_workspace_bytes(M, N, K)
+
+
+_types: dict = {}          # torch dtype -> (MQ_* code, bytes); filled on first use (torch loads late)
+
+
+def _dtype_code(dtype) -> int:
+    if not _types:
+        import torch
+        _types.update({torch.bfloat16: (BF16, 2), torch.float16: (F16, 2), torch.float32: (F32, 4)})
+    t = _types.get(dtype)
+    if t is None:
+        raise ValueError(f"dtype {dtype} is not one of bfloat16, float16, float32")
+    return t[0]
+
+
+def _rows(t, what: str, cols: int | None = None, rows: int | None = None) -> int:
+    """Check a 2-D device tensor whose rows are contiguous; its row stride."""
+    try:
+        n, k = t.shape
+        ld, one = t.stride()
+        cuda = t.is_cuda
+    except (AttributeError, TypeError, ValueError):
+        raise ValueError(f"{what} must be a 2-D tensor") from None
+    if not cuda:
+        raise ValueError(f"{what} must be on a GPU")
+    if (cols is not None and k != cols) or (rows is not None and n != rows):
+        raise ValueError(f"{what} has shape {(n, k)}, expected {(rows, cols)}")
+    if one != 1 and k > 1:
+        raise ValueError(f"{what} must have contiguous rows (stride 1 along the last axis)")
+    if n <= 1:
+        return k or 1
+    if ld < k:
+        raise ValueError(f"the rows of {what} overlap")
+    return ld
+
+
+class _On:
+    """`device` current and `stream` current for torch's allocator, so that what
+    a call allocates belongs to the stream it runs on."""
+
+    def __init__(self, device, stream):
+        import torch
+        if stream is None:
+            stream = torch.cuda.current_stream(device)
+        elif not isinstance(stream, torch.cuda.Stream):
+            ptr = getattr(stream, "cuda_stream", stream)
+            stream = torch.cuda.ExternalStream(int(ptr), device=device)
+        if stream.device != device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+        self._ctx = torch.cuda.stream(stream)
+        self.ptr = stream.cuda_stream
+
+    def __enter__(self):
+        self._ctx.__enter__()
+        return self.ptr
+
+    def __exit__(self, *exc):
+        return self._ctx.__exit__(*exc)
+
+
+class _Here:
+    """The common case of _On, without its cost (half the host time of a small
+    call): the current stream of the current device, nothing to switch."""
+
+    def __enter__(self):
+        return _raw_stream(self.index)
+
+    def __exit__(self, *exc):
+        return None
+
+
+_here = None
+_raw_stream = _get_device = None
+
+
+def _on(device, stream):
+    global _here, _raw_stream, _get_device
+    if _here is None:
+        import torch
+        _raw_stream, _get_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+        _here = {}
+    if stream is None and device.index == _get_device():
+        h = _here.get(device.index)
+        if h is None:
+            h = _Here()
+            h.index = device.index
+            _here[device.index] = h
+        return h
+    return _On(device, stream)
+
+
+class Mx4Matrix:
+    """A rows x K matrix in MXFP4 (device tensors): codes uint8 [rows, K/2] and
+    the scale blocks (mq_mx4 in include/mq.h)."""
+
+    __slots__ = ("rows", "K", "device", "struct", "_codes", "_scales", "_buf")
+
+    def __init__(self, codes, scales, rows: int, K: int):
+        import torch
+        for t, n, what in ((codes, mq_mx4_code_bytes(rows, K), "codes"),
+                           (scales, mq_mx4_scale_bytes(rows, K), "scales")):
+            if t.dtype != torch.uint8 or not t.is_cuda or not t.is_contiguous() or t.numel() != n:
+                raise ValueError(f"{what} must be {n} contiguous uint8 on a GPU")
+        if codes.device != scales.device:
+            raise ValueError("codes and scales are on different devices")
+        self.rows, self.K, self.device = rows, K, codes.device
+        self._codes, self._scales, self._buf = codes, scales, None
+        self.struct = MqMx4(codes.data_ptr(), scales.data_ptr(), rows, K)
+
+    @classmethod
+    def empty(cls, rows: int, K: int, device):
+        """Uninitialised buffers for a rows x K matrix."""
+        import torch
+        if rows < 0 or K < 32 or K % 32:
+            raise ValueError("need rows >= 0 and K a positive multiple of 32")
+        self = cls.__new__(cls)
+        # one allocation: the codes (rows of 16-byte multiples), then the scale blocks
+        nc, ns = rows * (K // 2), (rows + 127) // 128 * ((K + 127) // 128) * 512
+        buf = torch.empty(nc + ns, dtype=torch.uint8, device=device)
+        ptr = buf.data_ptr()
+        self.rows, self.K, self.device = rows, K, buf.device
+        self._codes = self._scales = None
+        self._buf = buf
+        self.struct = MqMx4(ptr, ptr + nc, rows, K)
+        return self
+
+    @property
+    def codes(self):
+        if self._codes is None:
+            self._codes = self._buf[:self.rows * (self.K // 2)].view(self.rows, self.K // 2)
+        return self._codes
+
+    @property
+    def scales(self):
+        if self._scales is None:
+            self._scales = self._buf[self.rows * (self.K // 2):]
+        return self._scales
+
+
+def _mx4_out(out, rows: int, K: int, device) -> Mx4Matrix:
+    if out is None:
+        return Mx4Matrix.empty(rows, K, device)
+    if (out.rows, out.K) != (rows, K) or out.device != device:
+        raise ValueError(f"out is {out.rows} x {out.K} on {out.device}, expected {rows} x {K} on {device}")
+    return out
+
+
+def mx4_quantize(X, out: Mx4Matrix | None = None, stream=None) -> Mx4Matrix:
+    """Rows of X (bf16, fp16 or fp32 [rows, K], K a multiple of 32) in MXFP4;
+    `out` (of the same size) receives them in place of new buffers."""
+    ld = _rows(X, "X")
+    rows, K = X.shape
+    dt = _dtype_code(X.dtype)
+    device = X.device
+    with _on(device, stream) as st:
+        out = _mx4_out(out, rows, K, device)
+        s = out.struct
+        _check(lib.mq_mx4_quantize(X.data_ptr(), dt, rows, K, ld, s.codes, s.scales, st))
+    return out
+
+
+def mx4_from_nested(weights: NestedWeights, r: int, out: Mx4Matrix | None = None, stream=None) -> Mx4Matrix:
+    """The r-bit model of a nested parent in MXFP4."""
+    w = weights.view(r)
+    device = weights.planes.device
+    with _on(device, stream) as st:
+        out = _mx4_out(out, weights.N, weights.K, device)
+        s = out.struct
+        _check(lib.mq_mx4_from_nested(w, s.codes, s.scales, st))
+    return out
+
+
+def mx4_dequantize(m: Mx4Matrix, dtype=None, out=None, stream=None):
+    """The values m stands for, bf16 (default) or fp32; both hold them exactly."""
+    import torch
+    if dtype is None:
+        dtype = out.dtype if out is not None else torch.bfloat16
+    dt = _dtype_code(dtype)
+    with _on(m.device, stream) as st:
+        if out is None:
+            out, ld = torch.empty((m.rows, m.K), dtype=dtype, device=m.device), m.K
+        else:
+            ld = _rows(out, "out", m.K, m.rows)
+            if out.dtype != dtype or out.device != m.device:
+                raise ValueError("out differs in dtype or device")
+        _check(lib.mq_mx4_dequantize(m.struct, out.data_ptr(), dt, ld, st))
+    return out
+
+
+def _mx4_y(Y, M: int, w: Mx4Matrix, dtype):
+    import torch
+    if dtype is None:
+        dtype = Y.dtype if Y is not None else torch.bfloat16
+    dt = _dtype_code(dtype)
+    if Y is None:
+        return torch.empty((M, w.rows), dtype=dtype, device=w.device), dt, w.rows
+    ldy = _rows(Y, "Y", w.rows, M)
+    if Y.dtype != dtype or Y.device != w.device:
+        raise ValueError("Y differs in dtype or device")
+    return Y, dt, ldy
+
+
+def mx4_gemm(X: Mx4Matrix, w: Mx4Matrix, Y=None, dtype=None, stream=None):
+    """Y = X . w^T, both in MXFP4 (X: M x K, w: N x K); Y bf16 (default), fp16
+    or fp32 [M, N]."""
+    if X.device != w.device:
+        raise ValueError("X and w are on different devices")
+    with _on(w.device, stream) as st:
+        Y, dt, ldy = _mx4_y(Y, X.rows, w, dtype)
+        _check(lib.mq_mx4_gemm(X.struct, w.struct, Y.data_ptr(), dt, ldy, st))
+    return Y
+
+
+def mx4_gemm_bf16(X, w: Mx4Matrix, Y=None, dtype=None, stream=None):
+    """Y = X . w^T with X in bf16 [M, K] as it is, w in MXFP4."""
+    import torch
+    ldx = _rows(X, "X", w.K)
+    if X.dtype != torch.bfloat16:
+        raise ValueError("X must be bfloat16")
+    if X.device != w.device:
+        raise ValueError("X and w are on different devices")
+    M = X.shape[0]
+    with _on(w.device, stream) as st:
+        Y, dt, ldy = _mx4_y(Y, M, w, dtype)
+        need = mq_mx4_gemm_bf16_workspace_bytes(M, w.rows, w.K)
+        ws = torch.empty(need, dtype=torch.uint8, device=w.device) if need else None
+        _check(lib.mq_mx4_gemm_bf16(X.data_ptr(), M, ldx, w.struct, Y.data_ptr(), dt, ldy,
+                                    ws.data_ptr() if ws is not None else None, need, st))
     return Y

@@ -50,7 +50,17 @@ mq_status bind_device(cudaStream_t st) {
     static thread_local cudaStream_t last_stream = nullptr;
     if (st != nullptr && st == last_stream) return MQ_OK;
     int dev = -1;
+    cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
     if (st != nullptr) {
+        cudaError_t e = cudaStreamIsCapturing(st, &cap);
+        if (e != cudaSuccess) return cuda_fail(e, "cudaStreamIsCapturing");
+    }
+    if (cap != cudaStreamCaptureStatusNone) {
+        // a capturing stream does not answer for its device (asking ends the
+        // capture): the caller's context, which captures on its own device
+        dev = current_context_device();
+        if (dev < 0) return MQ_OK;
+    } else if (st != nullptr) {
         cudaError_t e = cudaStreamGetDevice(st, &dev);
         if (e != cudaSuccess) return cuda_fail(e, "cudaStreamGetDevice");
     } else {
@@ -100,13 +110,6 @@ mq_status launch_small_m(const uint16_t *X, const mq_weights *w, int64_t M, uint
     if (!w->zeros && small_m_uses_gemv(M, w->N, w->K, w->r))
         return launch_gemv_tc(X, w, M, Y, ws, ws_bytes, st);
     return launch_gemm_tc(X, w, M, Y, ws, ws_bytes, st);
-}
-
-// fail() with a formatted message.
-template <class... A>
-mq_status failf(mq_status s, const char *fmt, A... args) {
-    set_error(s, fmt, args...);
-    return s;
 }
 
 }  // namespace mq
@@ -216,10 +219,10 @@ mq_status mq_last_error(void) { return g_last; }
 mq_status mq_device_status(void) {
     const cudaError_t e = cudaDeviceSynchronize();
     if (e != cudaSuccess) return cuda_fail(e, "cudaDeviceSynchronize");
-    bool a = false, b = false;
-    if (!gemv_tc_take_timeout(&a) || !gemm_tc_take_timeout(&b))
+    bool a = false, b = false, c = false;
+    if (!gemv_tc_take_timeout(&a) || !gemm_tc_take_timeout(&b) || !mx4_take_timeout(&c))
         return fail(MQ_ERR_CUDA, "device timeout flags not readable");
-    if (a || b) return fail(MQ_ERR_TIMEOUT, "a bounded device-side wait expired in an earlier launch");
+    if (a || b || c) return fail(MQ_ERR_TIMEOUT, "a bounded device-side wait expired in an earlier launch");
     return MQ_OK;
 }
 const char *mq_last_error_string(void) { return g_msg; }

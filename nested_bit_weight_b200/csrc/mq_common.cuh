@@ -27,6 +27,12 @@ inline mq_status fail(mq_status s, const char *what) {
     return s;
 }
 mq_status cuda_fail(cudaError_t e, const char *where);
+// fail() with a formatted message.
+template <class... A>
+mq_status failf(mq_status s, const char *fmt, A... args) {
+    set_error(s, fmt, args...);
+    return s;
+}
 
 // f() for the host-only entry points that allocate or start threads: no C++
 // exception crosses the C ABI (host memory exhausted, or threads refused,
@@ -60,6 +66,7 @@ bool gemv_tc_supported(int64_t M, int64_t N, int64_t K, int r);
 // Read and clear the device flag of a timed-out wait (false: device not readable).
 bool gemv_tc_take_timeout(bool *set);
 bool gemm_tc_take_timeout(bool *set);
+bool mx4_take_timeout(bool *set);
 size_t gemv_tc_workspace_bytes(int64_t M, int64_t N, int64_t K, int r);
 mq_status launch_gemv_tc(const uint16_t *X, const mq_weights *w, int64_t M,
                          uint16_t *Y, void *ws, size_t ws_bytes, cudaStream_t st);

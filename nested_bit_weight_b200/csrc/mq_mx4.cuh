@@ -1,0 +1,103 @@
+// MXFP4 (include/mq.h: e2m1 elements, one power-of-two scale per 32 columns):
+// the block arithmetic and the storage indices shared by the converters and
+// the products.
+#pragma once
+
+#include "mq_common.cuh"
+
+namespace mq {
+
+constexpr int kMxBlock = 32;                 // columns per scale
+constexpr int64_t kMxMaxDim = ((int64_t)1 << 31) - 256;   // rows and K (32-bit coordinates)
+
+// Validate an MXFP4 matrix; returns MQ_OK or the failing status.
+mq_status check_mx4(const mq_mx4 *m, const char *what);
+
+// Column groups of 128 (scale blocks of a row band).
+__host__ __device__ __forceinline__ int64_t mx_groups(int64_t K) { return (K + 127) / 128; }
+
+// Byte of the scales buffer that holds row `row`, columns 128 g .. 128 g + 31
+// (the three bytes behind it: the next 32 columns each).
+__host__ __device__ __forceinline__ int64_t mx_scale_at(int64_t row, int64_t g, int64_t G) {
+    return ((row >> 7) * G + g) * 512 + (row & 31) * 16 + ((row >> 5) & 3) * 4;
+}
+
+// Scale byte of a block whose largest magnitude has the bit pattern `amax`
+// (fp32, sign cleared): floor(log2 a) - 2 + 127, at least 0 (subnormal and
+// tiny blocks), 255 for a NaN or an infinity.
+__device__ __forceinline__ uint32_t mx_scale_byte(uint32_t amax) {
+    const uint32_t f = amax >> 23;
+    return f == 255u ? 255u : (f > 2u ? f - 2u : 0u);
+}
+
+// 2^(127 - E) for E <= 253.
+__device__ __forceinline__ float mx_inverse(uint32_t E) { return __uint_as_float((254u - E) << 23); }
+
+// 2^(E - 127), NaN for E = 255.
+__device__ __forceinline__ float mx_value(uint32_t E) {
+    return E == 0u ? __uint_as_float(0x00400000u) : E == 255u ? __uint_as_float(0x7FC00000u)
+                                                              : __uint_as_float(E << 23);
+}
+
+// Eight numbers, already divided by their scale, to eight codes (nearest,
+// ties to even, above 6 to 6), the first in the lowest bits.
+__device__ __forceinline__ uint32_t mx_codes8(const float (&u)[8]) {
+    uint32_t r;
+    asm("{\n .reg .b8 a, b, c, d;\n"
+        " cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n"
+        " cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n"
+        " cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n"
+        " cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n"
+        " mov.b32 %0, {a, b, c, d};\n}"
+        : "=r"(r)
+        : "f"(u[0]), "f"(u[1]), "f"(u[2]), "f"(u[3]), "f"(u[4]), "f"(u[5]), "f"(u[6]), "f"(u[7]));
+    return r;
+}
+
+// Eight codes to the numbers they stand for before scaling (exact in fp16).
+// Each byte is moved down by itself: taking the word apart with one
+// mov.b32 {a, b, c, d} loses the upper bytes when the word was put together
+// the same way just before (nvcc 12.9).
+__device__ __forceinline__ void mx_units8(uint32_t codes, float (&u)[8]) {
+    uint32_t h[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        asm("{\n .reg .b8 a;\n cvt.u8.u32 a, %1;\n cvt.rn.f16x2.e2m1x2 %0, a;\n}" : "=r"(h[i]) : "r"(codes >> (8 * i)));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h[i]));
+        u[2 * i] = f.x;
+        u[2 * i + 1] = f.y;
+    }
+}
+
+// ---- bf16 rows as sums of kMxSlices MXFP4 rows.  With a = max |x| of a
+// block, slice 0 has the least unit 2^e0 with a <= 7 * 2^e0: rounding to the
+// grid leaves at most 1 unit (up to 5 by half a step, above 5 to 6).  In units
+// a quarter as large that rest is at most 4, where the grid's half step is
+// 1/2; in units an eighth as large again at most 4, and so on.  After eight
+// slices the rest is at most 2^(e0 - 21), below 2^-22 a (a > 3.5 * 2^e0).
+constexpr int kMxSlices = 8;
+
+__device__ __forceinline__ uint32_t mx_slice0_byte(uint32_t amax) {
+    const uint32_t f = (amax >> 23) + ((amax & 0x7FFFFFu) > 0x600000u ? 1u : 0u);   // a > 1.75 * 2^k
+    return (amax >> 23) == 255u ? 255u : (f > 2u ? f - 2u : 0u);
+}
+// Scale byte of slice j + 1 from that of slice j (at least 0; 255 stays).
+__device__ __forceinline__ uint32_t mx_next_slice(uint32_t E, int j) {
+    const uint32_t d = j == 0 ? 2u : 3u;
+    return E == 255u ? 255u : (E > d ? E - d : 0u);
+}
+// Codes of one slice of eight numbers u (in the slice's unit); u becomes the
+// rest in the next slice's unit, 2^-step times as large.
+__device__ __forceinline__ uint32_t mx_slice_codes(float (&u)[8], uint32_t step) {
+    const uint32_t c = mx_codes8(u);
+    float q[8];
+    mx_units8(c, q);
+    const float f = __uint_as_float((127u + step) << 23);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) u[i] = (u[i] - q[i]) * f;
+    return c;
+}
+
+}  // namespace mq

@@ -197,6 +197,25 @@ __device__ __forceinline__ void mma_i8_ts(uint32_t d_tmem, uint32_t a_tmem, uint
         ::"r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate) : "memory");
 }
 
+// D[tmem] (+)= (A scaled)[smem] * (B scaled)[smem]^T, 4-bit floats (e2m1) with
+// one power-of-two scale (ue8m0) per 32 of K, 128 x N x 64, fp32 D; one thread.
+// sfa, sfb: tensor-memory columns of the scales (see tmem_cp_sf); the
+// instruction descriptor says which two of the four bytes apply.
+__device__ __forceinline__ void mma_mxf4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                         uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n}"
+        ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate) : "memory");
+}
+
+// Copy one 512-byte block of scales (32 rows of 16 bytes) from shared memory to
+// four tensor-memory columns, repeated in all four lane quarters; one thread,
+// in order before this thread's later MMAs.
+__device__ __forceinline__ void tmem_cp_sf(uint32_t taddr, uint64_t s_desc) {
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(s_desc) : "memory");
+}
+
 // Arrive on `bar` once all previously issued MMAs of this thread complete.
 __device__ __forceinline__ void mma_commit(uint64_t *bar) {
     asm volatile(
@@ -278,6 +297,14 @@ __device__ __forceinline__ void tma_load_3d(void *dst, const void *map, int x, i
         ::"r"(smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar)) : "memory");
 }
 
+// Tiled 2-D tensor copy (TMA), as tma_load_3d.
+__device__ __forceinline__ void tma_load_2d(void *dst, const void *map, int x, int y, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3}], [%4];"
+        ::"r"(smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar)) : "memory");
+}
+
 // Per-thread asynchronous copies global -> shared (4, 8 or 16 bytes, both
 // addresses aligned to the size), grouped per thread: commit closes a group,
 // wait<N> returns once at most N of this thread's newest groups are pending.
@@ -309,6 +336,16 @@ __device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t saddr) {
     return d;
 }
 
+// Shared-memory descriptor of a 512-byte block of scales: no swizzle, 8-row
+// groups of 16-byte rows 128 bytes apart.
+__device__ __forceinline__ uint64_t smem_desc_sf(uint32_t saddr) {
+    uint64_t d = 0;
+    d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);          // start address
+    d |= (uint64_t)(128 >> 4) << 32;                   // stride byte offset
+    d |= (uint64_t)1 << 46;                            // descriptor version (sm_100)
+    return d;
+}
+
 // Instruction descriptor: bf16 A and B (K-major), fp32 D, shape M x N.
 __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N) {
     return (1u << 4)                     // D format: f32
@@ -328,6 +365,19 @@ __host__ __device__ constexpr uint32_t idesc_u8s8(int N) {
          | ((uint32_t)(128 >> 4) << 24);  // M / 16
 }
 
+// Instruction descriptor: e2m1 A and B (K-major) with ue8m0 scales per 32 of
+// K, fp32 D, shape M x N x 64; `id` (0 or 2) is the first of the two scale
+// bytes used, for both operands.
+__host__ __device__ constexpr uint32_t idesc_mxf4(int M, int N, int id) {
+    return ((uint32_t)id << 4)            // B scale bytes
+         | (1u << 7)                      // A format: e2m1
+         | (1u << 10)                     // B format: e2m1
+         | ((uint32_t)(N >> 3) << 17)     // N / 8
+         | (1u << 23)                     // scale format: ue8m0
+         | ((uint32_t)(M >> 7) << 27)     // M / 128
+         | ((uint32_t)id << 29);          // A scale bytes
+}
+
 // Byte offset of 16-byte chunk `c` (0..7) of row `row` inside a 128-byte
 // swizzled K-major tile whose rows are 128 bytes.
 __host__ __device__ __forceinline__ uint32_t sw128_offset(uint32_t row, uint32_t c) {
@@ -340,6 +390,11 @@ __device__ __forceinline__ uint32_t cluster_map(uint32_t local, uint32_t rank) {
     uint32_t r;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(local), "r"(rank));
     return r;
+}
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
 }
 __device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
