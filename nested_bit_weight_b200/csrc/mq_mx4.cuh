@@ -3,6 +3,8 @@
 // the products.
 #pragma once
 
+#include <cuda.h>
+
 #include "mq_common.cuh"
 
 namespace mq {
@@ -12,6 +14,28 @@ constexpr int64_t kMxMaxDim = ((int64_t)1 << 31) - 256;   // rows and K (32-bit 
 
 // Validate an MXFP4 matrix; returns MQ_OK or the failing status.
 mq_status check_mx4(const mq_mx4 *m, const char *what);
+
+// Tensor map of codes (rows x K / 2 bytes) in boxes of 128 bytes x `box` rows,
+// 128-byte swizzle; bytes and rows beyond the matrix read as zeros.
+bool mx_encode_codes(CUtensorMap *map, const uint8_t *codes, int64_t rows, int64_t K, int box);
+// Tensor map of Y (M x N of type `out`, row stride ldy) in boxes of 128 bytes x 32
+// rows, 128-byte swizzle; the row stride must be a multiple of 16 bytes.
+bool mx_encode_y(CUtensorMap *map, void *Y, int64_t M, int64_t N, int64_t ldy, int out);
+
+// One product: X of M * slices MXFP4 rows (slices > 1: sums of that many
+// consecutive rows, mq_mx4_gemm_bf16), w of N rows.
+struct MxProduct {
+    const uint8_t *xcodes, *xscales;
+    int64_t M;
+    int slices;
+    const mq_mx4 *w;
+    void *Y;
+    int out;
+    int64_t ldy;
+};
+bool mx_pair_takes(const MxProduct &p);
+mq_status launch_mx_pair(const MxProduct &p, cudaStream_t st);
+bool mx_pair_take_timeout(bool *set);
 
 // Column groups of 128 (scale blocks of a row band).
 __host__ __device__ __forceinline__ int64_t mx_groups(int64_t K) { return (K + 127) / 128; }

@@ -254,32 +254,6 @@ mx4_gemm_kernel(const __grid_constant__ MxArgs a) {
     }
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 encoder() {
-    static std::atomic<void *> cached{nullptr};
-    void *f = cached.load(std::memory_order_acquire);
-    if (!f) {
-        cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) != cudaSuccess ||
-            q != cudaDriverEntryPointSuccess)
-            return nullptr;
-        cached.store(f, std::memory_order_release);
-    }
-    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-}
-
-// Codes (rows x K / 2 bytes) in boxes of 128 bytes x box rows, 128-byte
-// swizzle; bytes and rows beyond the matrix read as zeros.
-bool encode_codes(CUtensorMap *map, const uint8_t *codes, int64_t rows, int64_t K, int box) {
-    PFN_cuTensorMapEncodeTiled_v12000 enc = encoder();
-    if (!enc) return false;
-    const cuuint64_t dims[2] = {(cuuint64_t)(K / 2), (cuuint64_t)rows};
-    const cuuint64_t strides[1] = {(cuuint64_t)(K / 2)};
-    const cuuint32_t boxes[2] = {128, (cuuint32_t)box}, estr[2] = {1, 1};
-    return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t *>(codes), dims, strides, boxes, estr,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 using MxFn = void (*)(MxArgs);
 
 template <int BN>
@@ -297,10 +271,10 @@ cudaError_t pick(MxFn *fn, size_t *smem) {
     return e;
 }
 
-// Both operands in MXFP4; X has M * slices rows.
-mq_status launch(const uint8_t *xcodes, const uint8_t *xscales, int64_t M, int slices, const mq_mx4 *w, void *Y,
-                 int out, int64_t ldy, cudaStream_t st) {
-    const int64_t cols = M * slices;
+mq_status launch(const MxProduct &p, cudaStream_t st) {
+    if (mx_pair_takes(p)) return launch_mx_pair(p, st);
+    const mq_mx4 *w = p.w;
+    const int64_t cols = p.M * p.slices;
     const int BN = cols <= 8 ? 8 : cols <= 16 ? 16 : cols <= 32 ? 32 : cols <= 64 ? 64 : cols <= 128 ? 128 : 256;
     MxFn fn;
     size_t smem;
@@ -312,20 +286,21 @@ mq_status launch(const uint8_t *xcodes, const uint8_t *xscales, int64_t M, int s
                                        : pick<256>(&fn, &smem);
     if (pe != cudaSuccess) return cuda_fail(pe, "cudaFuncSetAttribute");
     MxArgs a{};
-    if (!encode_codes(&a.wmap, w->codes, w->rows, w->K, kTileN) || !encode_codes(&a.xmap, xcodes, cols, w->K, BN))
+    if (!mx_encode_codes(&a.wmap, w->codes, w->rows, w->K, kTileN) ||
+        !mx_encode_codes(&a.xmap, p.xcodes, cols, w->K, BN))
         return fail(MQ_ERR_CUDA, "cuTensorMapEncodeTiled (MXFP4 codes)");
     a.ws = w->scales;
-    a.xs = xscales;
-    a.Y = Y;
-    a.ldy = ldy;
-    a.M = (int)M;
+    a.xs = p.xscales;
+    a.Y = p.Y;
+    a.ldy = p.ldy;
+    a.M = (int)p.M;
     a.N = (int)w->rows;
     a.K = w->K;
     a.G = mx_groups(w->K);
     a.MB = (int)((cols + BN - 1) / BN);
     a.KT = (int)((w->K + kTileK - 1) / kTileK);
-    a.slices = slices;
-    a.out = out;
+    a.slices = p.slices;
+    a.out = p.out;
     const int64_t tiles = (w->rows + kTileN - 1) / kTileN * a.MB;
     // K is split while the CTAs still fit the GPU once and each keeps two
     // stages of K
@@ -365,11 +340,51 @@ size_t slice_code_bytes(int64_t M, int64_t K) {
 
 }  // namespace
 
+PFN_cuTensorMapEncodeTiled_v12000 mx_encoder() {
+    static std::atomic<void *> cached{nullptr};
+    void *f = cached.load(std::memory_order_acquire);
+    if (!f) {
+        cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            return nullptr;
+        cached.store(f, std::memory_order_release);
+    }
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+}
+
+bool mx_encode_codes(CUtensorMap *map, const uint8_t *codes, int64_t rows, int64_t K, int box) {
+    PFN_cuTensorMapEncodeTiled_v12000 enc = mx_encoder();
+    if (!enc) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)(K / 2), (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)(K / 2)};
+    const cuuint32_t boxes[2] = {128, (cuuint32_t)box}, estr[2] = {1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t *>(codes), dims, strides, boxes, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool mx_encode_y(CUtensorMap *map, void *Y, int64_t M, int64_t N, int64_t ldy, int out) {
+    PFN_cuTensorMapEncodeTiled_v12000 enc = mx_encoder();
+    if (!enc) return false;
+    const int size = out == MQ_F32 ? 4 : 2;
+    const cuuint64_t dims[2] = {(cuuint64_t)N, (cuuint64_t)M};
+    const cuuint64_t strides[1] = {(cuuint64_t)(ldy * size)};
+    const cuuint32_t boxes[2] = {(cuuint32_t)(128 / size), 32}, estr[2] = {1, 1};
+    const CUtensorMapDataType t = out == MQ_F32   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                  : out == MQ_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                  : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    return enc(map, t, 2, Y, dims, strides, boxes, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool mx4_take_timeout(bool *set) {
     unsigned v = 0, z = 0;
+    bool pair = false;
+    if (!mx_pair_take_timeout(&pair)) return false;
     if (cudaMemcpyFromSymbol(&v, g_mx_timeout, sizeof(v)) != cudaSuccess) return false;
     if (v && cudaMemcpyToSymbol(g_mx_timeout, &z, sizeof(z)) != cudaSuccess) return false;
-    *set = v != 0;
+    *set = v != 0 || pair;
     return true;
 }
 
@@ -388,7 +403,7 @@ extern "C" mq_status mq_mx4_gemm(const mq_mx4 *X, const mq_mx4 *w, void *Y, int 
     if ((s = check_y("mq_mx4_gemm", w->rows, Y, y_dtype, ldy)) != MQ_OK) return s;
     cudaStream_t st = (cudaStream_t)stream;
     if ((s = bind_device(st)) != MQ_OK) return s;
-    return launch(X->codes, X->scales, X->rows, 1, w, Y, y_dtype, ldy, st);
+    return launch(MxProduct{X->codes, X->scales, X->rows, 1, w, Y, y_dtype, ldy}, st);
 }
 
 extern "C" size_t mq_mx4_gemm_bf16_workspace_bytes(int64_t M, int64_t N, int64_t K) {
@@ -417,12 +432,16 @@ extern "C" mq_status mq_mx4_gemm_bf16(const uint16_t *X, int64_t M, int64_t ldx,
     if ((s = bind_device(st)) != MQ_OK) return s;
     uint8_t *codes = static_cast<uint8_t *>(workspace), *scales = codes + slice_code_bytes(M, w->K);
     if ((s = launch_mx_slices(X, M, w->K, ldx, codes, scales, st)) != MQ_OK) return s;
-    return launch(codes, scales, M, kMxSlices, w, Y, y_dtype, ldy, st);
+    return launch(MxProduct{codes, scales, M, kMxSlices, w, Y, y_dtype, ldy}, st);
 }
 
 #ifdef MQ_TEST_HOOKS
 // Test-hook builds only: make the next `n` CTAs of an MXFP4 product drop their loads.
+namespace mq {
+int pair_test_drop(int n);
+}
 extern "C" __attribute__((visibility("default"))) int mq_test_drop_mx4_loads(int n) {
-    return (int)cudaMemcpyToSymbol(mq::g_test_drop_mx4, &n, sizeof(n));
+    const int e = mq::pair_test_drop(n);
+    return e ? e : (int)cudaMemcpyToSymbol(mq::g_test_drop_mx4, &n, sizeof(n));
 }
 #endif
