@@ -126,17 +126,21 @@ mx4_gemm_kernel(const __grid_constant__ MxArgs a) {
 
     if (warp == 0) {
         // -------------------------------------------------------------- loads
-        if (lane == 0) {
-            const int64_t xband = (int64_t)mb * BN / 128, xbands = ((int64_t)a.M * a.slices + 127) / 128;
-            for (int i = 0; i < k1 - k0; ++i) {
-                const int st = i % kS, kt = k0 + i;
+        const int64_t xband = (int64_t)mb * BN / 128, xbands = ((int64_t)a.M * a.slices + 127) / 128;
+        const int bands = xbands - xband < C::kBands ? (int)(xbands - xband) : C::kBands;
+        for (int i = 0; i < k1 - k0; ++i) {
+            const int st = i % kS, kt = k0 + i;
 #ifdef MQ_TEST_HOOKS
-                if (i == 0 && atomicSub(&g_test_drop_mx4, 1) > 0) break;
+            if (i == 0) {
+                const int drop = lane == 0 ? atomicSub(&g_test_drop_mx4, 1) : 0;
+                if (__any_sync(0xFFFFFFFFu, drop > 0)) break;
+            }
 #endif
-                if (i >= kS && !mbar_wait_backoff(empty + st, (uint32_t)(i / kS - 1) & 1u, flags)) break;
+            const bool ok = i < kS || mbar_wait_backoff(empty + st, (uint32_t)(i / kS - 1) & 1u, flags);
+            if (!__all_sync(0xFFFFFFFFu, ok)) break;
+            if (elect_one()) {
                 uint8_t *sA = smem + st * C::kStage, *sB = sA + C::kA, *sfA = sB + C::kB, *sfB = sfA + C::kSfA;
                 const uint32_t sfbytes = 512u * (uint32_t)(a.G - 2 * kt < 2 ? a.G - 2 * kt : 2);
-                const int bands = xbands - xband < C::kBands ? (int)(xbands - xband) : C::kBands;
                 mbar_expect_tx(full + st, C::kA + C::kB + sfbytes * (1 + bands));
                 tma_load_2d(sA, &a.wmap, kt * 128, t * kTileN, full + st);
                 tma_load_2d(sB, &a.xmap, kt * 128, mb * BN, full + st);
@@ -145,34 +149,41 @@ mx4_gemm_kernel(const __grid_constant__ MxArgs a) {
                     bulk_g2s(sfB + b * 1024, a.xs + ((xband + b) * a.G + 2 * kt) * 512, sfbytes, full + st);
                 flags[1] = i + 1;
             }
+            __syncwarp();
         }
     } else if (warp == 1) {
         // --------------------------------------------------------------- MMAs
-        if (lane == 0) {
-            for (int i = 0; i < k1 - k0; ++i) {
-                const int st = i % kS;
-                if (!mbar_wait_abortable(full + st, (uint32_t)(i / kS) & 1u, flags)) break;
-                tc_fence_after();
+        for (int i = 0; i < k1 - k0; ++i) {
+            const int st = i % kS;
+            const bool ok = mbar_wait_abortable(full + st, (uint32_t)(i / kS) & 1u, flags);
+            if (!__all_sync(0xFFFFFFFFu, ok)) break;
+            tc_fence_after();
+            const int64_t left = a.K - (int64_t)(k0 + i) * kTileK;
+            if (elect_one()) {
                 const uint32_t sA = smem_u32(smem + st * C::kStage), sB = sA + C::kA, sfA = sB + C::kB,
                                sfB = sfA + C::kSfA;
                 const uint32_t tA = tmem + C::kSf + st * C::kSfCols, tB = tA + 8;
-                const int64_t left = a.K - (int64_t)(k0 + i) * kTileK;
+                const uint64_t ad = smem_desc_sw128(sA), bd = smem_desc_sw128(sB);
                 const int steps = left >= kTileK ? 4 : (int)((left + 63) / 64);
                 // scales: four columns per 128 rows and group
-                for (int g = 0; 2 * g < steps; ++g) {
-                    tmem_cp_sf(tA + 4 * g, smem_desc_sf(sfA + 512 * g));
 #pragma unroll
-                    for (int b = 0; b < C::kBands; ++b)
-                        tmem_cp_sf(tB + 4 * (C::kBands * g + b), smem_desc_sf(sfB + 1024 * b + 512 * g));
-                }
-                const uint64_t ad = smem_desc_sw128(sA), bd = smem_desc_sw128(sB);
-                for (int j = 0; j < steps; ++j)
-                    mma_mxf4(tmem + C::kD, ad + 2 * j, bd + 2 * j, idesc_mxf4(kTileN, BN, (j & 1) * 2),
-                             tA + 4 * (j >> 1), tB + 4 * C::kBands * (j >> 1), i + j > 0 ? 1u : 0u);
+                for (int g = 0; g < 2; ++g)
+                    if (2 * g < steps) {
+                        tmem_cp_sf(tA + 4 * g, smem_desc_sf(sfA + 512 * g));
+#pragma unroll
+                        for (int b = 0; b < C::kBands; ++b)
+                            tmem_cp_sf(tB + 4 * (C::kBands * g + b), smem_desc_sf(sfB + 1024 * b + 512 * g));
+                    }
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (j < steps)
+                        mma_mxf4(tmem + C::kD, ad + 2 * j, bd + 2 * j, idesc_mxf4(kTileN, BN, (j & 1) * 2),
+                                 tA + 4 * (j >> 1), tB + 4 * C::kBands * (j >> 1), i + j > 0 ? 1u : 0u);
                 mma_commit(empty + st);
+                if (i == k1 - k0 - 1) mma_commit(done);
                 flags[2] = i + 1;
             }
-            if (flags[2] == k1 - k0) mma_commit(done);
+            __syncwarp();
         }
     }
     __syncwarp();

@@ -170,23 +170,24 @@ mx4_pair_kernel(const __grid_constant__ PairArgs a) {
 
     if (warp == 0) {
         // -------------------------------------------------------------- loads
-        if (lane == 0) {
-            int i = 0;                                               // stages over all tiles
-            bool ok = true;
-            for (int tile = cluster; tile < tiles && ok; tile += nclusters) {
-                const int ta = tile % a.Ta, tb = tile / a.Ta;
-                const int64_t band_a = (int64_t)ta * 2 + rank, band_b = (int64_t)tb * C::kBands;
-                const bool has_a = band_a < a.a_bands;
-                const int nb = a.b_bands - band_b < C::kBands ? (int)(a.b_bands - band_b) : C::kBands;
-                for (int kt = 0; kt < a.KT; ++kt, ++i) {
-                    const int st = i % kS;
+        int i = 0;                                                   // stages over all tiles
+        bool ok = true;
+        for (int tile = cluster; tile < tiles && ok; tile += nclusters) {
+            const int ta = tile % a.Ta, tb = tile / a.Ta;
+            const int64_t band_a = (int64_t)ta * 2 + rank, band_b = (int64_t)tb * C::kBands;
+            const bool has_a = band_a < a.a_bands;
+            const int nb = a.b_bands - band_b < C::kBands ? (int)(a.b_bands - band_b) : C::kBands;
+            for (int kt = 0; kt < a.KT; ++kt, ++i) {
+                const int st = i % kS;
 #ifdef MQ_TEST_HOOKS
-                    if (i == 0 && atomicSub(&g_test_drop_pair, 1) > 0) { ok = false; break; }
+                if (i == 0) {
+                    const int drop = lane == 0 ? atomicSub(&g_test_drop_pair, 1) : 0;
+                    if (__any_sync(0xFFFFFFFFu, drop > 0)) { ok = false; break; }
+                }
 #endif
-                    if (i >= kS && !mbar_wait_backoff(empty + st, (uint32_t)(i / kS - 1) & 1u, flags)) {
-                        ok = false;
-                        break;
-                    }
+                ok = i < kS || mbar_wait_backoff(empty + st, (uint32_t)(i / kS - 1) & 1u, flags);
+                if (!(ok = __all_sync(0xFFFFFFFFu, ok))) break;
+                if (elect_one()) {
                     uint8_t *sA = smem + st * C::kStage, *sB = sA + C::kA, *sfA = sB + C::kB, *sfB = sfA + C::kSfA;
                     const uint32_t sfbytes = 512u * (uint32_t)(a.G - 2 * kt < 2 ? a.G - 2 * kt : 2);
                     mbar_expect_tx(full + st, C::kA + C::kB + sfbytes * (uint32_t)(nb + (has_a ? 1 : 0)));
@@ -197,61 +198,67 @@ mx4_pair_kernel(const __grid_constant__ PairArgs a) {
                         bulk_g2s(sfB + b * 1024, a.bs + ((band_b + b) * a.G + 2 * kt) * 512, sfbytes, full + st);
                     flags[1] = i + 1;
                 }
+                __syncwarp();
             }
         }
+    } else if (warp == 1 && rank == 1) {
+        // ----------------------------------------- this CTA's stages have arrived
+        int i = 0;
+        bool ok = true;
+        const uint32_t there = cluster_map(smem_u32(peer), 0);
+        for (int tile = cluster; tile < tiles && ok; tile += nclusters)
+            for (int kt = 0; kt < a.KT; ++kt, ++i) {
+                ok = mbar_wait_abortable(full + i % kS, (uint32_t)(i / kS) & 1u, flags);
+                if (!(ok = __all_sync(0xFFFFFFFFu, ok))) break;
+                if (elect_one()) mbar_arrive_remote(there + 8u * (uint32_t)(i % kS));
+                __syncwarp();
+            }
     } else if (warp == 1) {
-        if (lane == 0 && rank == 1) {
-            // ------------------------------------- this CTA's stages have arrived
-            int i = 0;
-            bool ok = true;
-            const uint32_t there = cluster_map(smem_u32(peer), 0);
-            for (int tile = cluster; tile < tiles && ok; tile += nclusters)
-                for (int kt = 0; kt < a.KT; ++kt, ++i) {
-                    if (!mbar_wait_abortable(full + i % kS, (uint32_t)(i / kS) & 1u, flags)) {
-                        ok = false;
-                        break;
-                    }
-                    mbar_arrive_remote(there + 8u * (uint32_t)(i % kS));
-                }
-        } else if (lane == 0) {
-            // ---------------------------------------------------------- MMAs
-            int i = 0, it = 0;
-            bool ok = true;
-            for (int tile = cluster; tile < tiles && ok; tile += nclusters, ++it) {
-                if (it >= C::kLag) {
-                    const int w = it - C::kLag;
-                    if (!mbar_wait_cluster_abortable(dfree + (w & 1), (uint32_t)(w >> 1) & 1u, flags)) break;
-                }
+        // --------------------------------------------------------------- MMAs
+        int i = 0, it = 0;
+        bool ok = true;
+        for (int tile = cluster; tile < tiles && ok; tile += nclusters, ++it) {
+            if (it >= C::kLag) {
+                const int w = it - C::kLag;
+                ok = mbar_wait_cluster_abortable(dfree + (w & 1), (uint32_t)(w >> 1) & 1u, flags);
+                if (!(ok = __all_sync(0xFFFFFFFFu, ok))) break;
+            }
+            const uint32_t d = tmem + (it & 1 ? C::kD1 : 0u);
+            for (int kt = 0; kt < a.KT; ++kt, ++i) {
+                const int st = i % kS;
+                // the stage is in both CTAs' shared memory, and the MMAs that
+                // read this half of the scale columns are done
+                ok = mbar_wait_abortable(full + st, (uint32_t)(i / kS) & 1u, flags) &&
+                     mbar_wait_cluster_abortable(peer + st, (uint32_t)(i / kS) & 1u, flags) &&
+                     (i < 2 || mbar_wait_abortable(empty + (i - 2) % kS, (uint32_t)((i - 2) / kS) & 1u, flags));
+                if (!(ok = __all_sync(0xFFFFFFFFu, ok))) break;
                 tc_fence_after();
-                const uint32_t d = tmem + (it & 1 ? C::kD1 : 0u);
-                for (int kt = 0; kt < a.KT; ++kt, ++i) {
-                    const int st = i % kS;
-                    // the stage is in both CTAs' shared memory, and the MMAs that
-                    // read this half of the scale columns are done
-                    ok = mbar_wait_abortable(full + st, (uint32_t)(i / kS) & 1u, flags) &&
-                         mbar_wait_cluster_abortable(peer + st, (uint32_t)(i / kS) & 1u, flags) &&
-                         (i < 2 || mbar_wait_abortable(empty + (i - 2) % kS, (uint32_t)((i - 2) / kS) & 1u, flags));
-                    if (!ok) break;
-                    tc_fence_after();
+                const int64_t left = a.K - (int64_t)kt * kTileK;
+                if (elect_one()) {
                     const uint32_t sA = smem_u32(smem + st * C::kStage), sB = sA + C::kA, sfA = sB + C::kB,
                                    sfB = sfA + C::kSfA;
                     const uint32_t tA = tmem + C::kSf + (uint32_t)(i & 1) * C::kSfCols, tB = tA + 8;
-                    const int64_t left = a.K - (int64_t)kt * kTileK;
-                    const int steps = left >= kTileK ? 4 : (int)((left + 63) / 64);
-                    for (int g = 0; 2 * g < steps; ++g) {
-                        tmem_cp_sf_pair(tA + 4 * g, smem_desc_sf(sfA + 512 * g));
-#pragma unroll
-                        for (int b = 0; b < C::kBands; ++b)
-                            tmem_cp_sf_pair(tB + 4 * (C::kBands * g + b), smem_desc_sf(sfB + 1024 * b + 512 * g));
-                    }
                     const uint64_t ad = smem_desc_sw128(sA), bd = smem_desc_sw128(sB);
-                    for (int j = 0; j < steps; ++j)
-                        mma_mxf4_pair(d, ad + 2 * j, bd + 2 * j, idesc_mxf4(256, BN, (j & 1) * 2), tA + 4 * (j >> 1),
-                                      tB + 4 * C::kBands * (j >> 1), kt + j > 0 ? 1u : 0u);
+                    const int steps = left >= kTileK ? 4 : (int)((left + 63) / 64);
+                    // scales: four columns per 128 rows and group
+#pragma unroll
+                    for (int g = 0; g < 2; ++g)
+                        if (2 * g < steps) {
+                            tmem_cp_sf_pair(tA + 4 * g, smem_desc_sf(sfA + 512 * g));
+#pragma unroll
+                            for (int b = 0; b < C::kBands; ++b)
+                                tmem_cp_sf_pair(tB + 4 * (C::kBands * g + b), smem_desc_sf(sfB + 1024 * b + 512 * g));
+                        }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (j < steps)
+                            mma_mxf4_pair(d, ad + 2 * j, bd + 2 * j, idesc_mxf4(256, BN, (j & 1) * 2),
+                                          tA + 4 * (j >> 1), tB + 4 * C::kBands * (j >> 1), kt + j > 0 ? 1u : 0u);
                     mma_commit_pair(empty + st);
+                    if (kt == a.KT - 1) mma_commit_pair(dfull + (it & 1));
                     flags[2] = i + 1;
                 }
-                if (ok) mma_commit_pair(dfull + (it & 1));
+                __syncwarp();
             }
         }
     } else {
