@@ -18,6 +18,9 @@ mq_status check_mx4(const mq_mx4 *m, const char *what);
 // Tensor map of codes (rows x K / 2 bytes) in boxes of 128 bytes x `box` rows,
 // 128-byte swizzle; bytes and rows beyond the matrix read as zeros.
 bool mx_encode_codes(CUtensorMap *map, const uint8_t *codes, int64_t rows, int64_t K, int box);
+// Tensor map of scale blocks (`rows` matrix rows) in boxes of two blocks x `box`
+// row bands (1024 bytes a band); blocks beyond the buffer read as zeros.
+bool mx_encode_scales(CUtensorMap *map, const uint8_t *scales, int64_t rows, int64_t K, int box);
 // Tensor map of Y (M x N of type `out`, row stride ldy) in boxes of 128 bytes x 32
 // rows, 128-byte swizzle; the row stride must be a multiple of 16 bytes.
 bool mx_encode_y(CUtensorMap *map, void *Y, int64_t M, int64_t N, int64_t ldy, int out);

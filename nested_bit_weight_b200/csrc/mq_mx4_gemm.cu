@@ -375,6 +375,18 @@ bool mx_encode_codes(CUtensorMap *map, const uint8_t *codes, int64_t rows, int64
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool mx_encode_scales(CUtensorMap *map, const uint8_t *scales, int64_t rows, int64_t K, int box) {
+    PFN_cuTensorMapEncodeTiled_v12000 enc = mx_encoder();
+    if (!enc) return false;
+    const int64_t G = mx_groups(K);
+    const cuuint64_t dims[2] = {(cuuint64_t)G * 128, (cuuint64_t)((rows + 127) / 128)};
+    const cuuint64_t strides[1] = {(cuuint64_t)G * 512};
+    const cuuint32_t boxes[2] = {256, (cuuint32_t)box}, estr[2] = {1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<uint8_t *>(scales), dims, strides, boxes, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool mx_encode_y(CUtensorMap *map, void *Y, int64_t M, int64_t N, int64_t ldy, int out) {
     PFN_cuTensorMapEncodeTiled_v12000 enc = mx_encoder();
     if (!enc) return false;

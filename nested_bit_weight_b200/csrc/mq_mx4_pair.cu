@@ -12,14 +12,15 @@
 //
 // Persistent clusters, tiles dealt in turn (rows of A fastest, so that the
 // clusters at work share B tiles in L2).  Tensor memory: two accumulators and
-// two stages of scales.  Two 256-column accumulators and the scales do not fit
-// 512 columns, so the accumulators overlap by 64 columns (0..255, 192..447);
-// the epilogue reads those first and lets the next tile's MMAs start.
+// the scales of every stage of the shared-memory ring (a stage's scales are
+// overwritten only once its MMAs are done, with no wait of their own).  That is
+// more than 512 columns, so the accumulators overlap by half (0..255, 128..383);
+// the epilogue reads the shared half first and lets the next tile's MMAs start.
 //
-// Roles: a loading thread; in the even CTA the thread that issues MMAs, in the
-// odd CTA one that tells the even CTA's that its stage has arrived; four
-// epilogue warps.  Waits are bounded as in the other kernels, and a cluster
-// barrier at the end keeps a CTA until its peer is through.
+// Roles: a loading warp (both CTAs' loads complete on the even CTA's barrier), a
+// warp of the even CTA that issues the MMAs, four epilogue warps.  Waits are
+// bounded as in the other kernels, and a cluster barrier at the end keeps a
+// CTA until its peer is through.
 #include <cuda.h>
 
 #include <atomic>
@@ -51,22 +52,21 @@ struct PairCfg {
     static constexpr int kStages = BN == 256 ? 5 : 7;
     static constexpr uint32_t kStg = 4096;                           // one 32-row piece of Y
     static constexpr int kLag = BN == 256 ? 1 : 2;                   // tiles until the accumulator is needed again
-    static constexpr uint32_t kD1 = BN == 256 ? 192 : BN;            // second accumulator
-    static constexpr uint32_t kSf = 448, kSfCols = 8 + 8 * kBands;   // scales: two stages
-    static_assert(kD1 + BN <= kSf && kSf + 2 * kSfCols <= 512, "TMEM columns");
+    static constexpr uint32_t kD1 = 128;                             // second accumulator
+    static constexpr uint32_t kSf = kD1 + BN, kSfCols = 8 + 8 * kBands;
+    static_assert(kSf + kStages * kSfCols <= 512, "TMEM columns");
     static constexpr size_t kSmem = 1024 + (size_t)kStages * kStage + 8 * kStg + 512;
     static_assert(kSmem <= 227 * 1024 && kStage % 1024 == 0, "shared memory");
 };
 
 struct PairArgs {
     CUtensorMap amap, bmap, ymap;  // codes in boxes of 128 and BN / 2 rows; Y
-    const uint8_t *as, *bs;        // scales
+    CUtensorMap asmap, bsmap;      // scales in boxes of 1 and BN / 128 row bands
     void *Y;
     int64_t ldy;
     int M, N;                      // rows of Y, columns of Y
-    int64_t K, G;
+    int64_t K;
     int Ta, Tb, KT;                // tiles along A and B, K tiles
-    int64_t a_bands, b_bands;      // 128-row scale bands of A and B
     int out;
     int tma_y;                     // Y's rows allow TMA stores
 };
@@ -135,8 +135,8 @@ mx4_pair_kernel(const __grid_constant__ PairArgs a) {
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint8_t *stg = smem + kS * C::kStage;                            // [warp][2][4096]
     uint64_t *full = reinterpret_cast<uint64_t *>(stg + 8 * C::kStg);
-    uint64_t *peer = full + kS, *empty = peer + kS, *dfull = empty + kS, *dfree = dfull + 2;
-    volatile int *flags = reinterpret_cast<volatile int *>(dfree + 2);   // [0] abort [1] loads [2] MMA stages
+    uint64_t *empty = full + kS, *dfull = empty + kS, *dfree = dfull + 2;
+    volatile int *flags = reinterpret_cast<volatile int *>(dfree + 2);   // [0] abort [2] MMA stages
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(dfree + 2) + 4;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -146,14 +146,13 @@ mx4_pair_kernel(const __grid_constant__ PairArgs a) {
     if (threadIdx.x == 0) {
         for (int i = 0; i < kS; ++i) {
             mbar_init(full + i, 1);
-            mbar_init(peer + i, 1);
             mbar_init(empty + i, 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(dfull + i, 1);
             mbar_init(dfree + i, 8);                                 // four epilogue warps of each CTA
         }
-        flags[0] = flags[1] = flags[2] = 0;
+        flags[0] = flags[2] = 0;
         fence_mbar_init();
     }
     pdl_wait();
@@ -172,11 +171,9 @@ mx4_pair_kernel(const __grid_constant__ PairArgs a) {
         // -------------------------------------------------------------- loads
         int i = 0;                                                   // stages over all tiles
         bool ok = true;
+        const uint32_t full0 = cluster_map(smem_u32(full), 0);       // the even CTA's barriers
         for (int tile = cluster; tile < tiles && ok; tile += nclusters) {
             const int ta = tile % a.Ta, tb = tile / a.Ta;
-            const int64_t band_a = (int64_t)ta * 2 + rank, band_b = (int64_t)tb * C::kBands;
-            const bool has_a = band_a < a.a_bands;
-            const int nb = a.b_bands - band_b < C::kBands ? (int)(a.b_bands - band_b) : C::kBands;
             for (int kt = 0; kt < a.KT; ++kt, ++i) {
                 const int st = i % kS;
 #ifdef MQ_TEST_HOOKS
@@ -189,31 +186,17 @@ mx4_pair_kernel(const __grid_constant__ PairArgs a) {
                 if (!(ok = __all_sync(0xFFFFFFFFu, ok))) break;
                 if (elect_one()) {
                     uint8_t *sA = smem + st * C::kStage, *sB = sA + C::kA, *sfA = sB + C::kB, *sfB = sfA + C::kSfA;
-                    const uint32_t sfbytes = 512u * (uint32_t)(a.G - 2 * kt < 2 ? a.G - 2 * kt : 2);
-                    mbar_expect_tx(full + st, C::kA + C::kB + sfbytes * (uint32_t)(nb + (has_a ? 1 : 0)));
-                    tma_load_2d(sA, &a.amap, kt * 128, ta * 256 + rank * 128, full + st);
-                    tma_load_2d(sB, &a.bmap, kt * 128, tb * BN + rank * (BN / 2), full + st);
-                    if (has_a) bulk_g2s(sfA, a.as + (band_a * a.G + 2 * kt) * 512, sfbytes, full + st);
-                    for (int b = 0; b < nb; ++b)
-                        bulk_g2s(sfB + b * 1024, a.bs + ((band_b + b) * a.G + 2 * kt) * 512, sfbytes, full + st);
-                    flags[1] = i + 1;
+                    const uint32_t bar = full0 + 8u * (uint32_t)st;
+                    if (rank == 0) mbar_expect_tx(full + st, 2 * C::kStage);
+                    tma_load_2d_pair(sA, &a.amap, kt * 128, ta * 256 + rank * 128, bar);
+                    tma_load_2d_pair(sB, &a.bmap, kt * 128, tb * BN + rank * (BN / 2), bar);
+                    tma_load_2d_pair(sfA, &a.asmap, kt * 256, ta * 2 + rank, bar);
+                    tma_load_2d_pair(sfB, &a.bsmap, kt * 256, tb * C::kBands, bar);
                 }
                 __syncwarp();
             }
         }
-    } else if (warp == 1 && rank == 1) {
-        // ----------------------------------------- this CTA's stages have arrived
-        int i = 0;
-        bool ok = true;
-        const uint32_t there = cluster_map(smem_u32(peer), 0);
-        for (int tile = cluster; tile < tiles && ok; tile += nclusters)
-            for (int kt = 0; kt < a.KT; ++kt, ++i) {
-                ok = mbar_wait_abortable(full + i % kS, (uint32_t)(i / kS) & 1u, flags);
-                if (!(ok = __all_sync(0xFFFFFFFFu, ok))) break;
-                if (elect_one()) mbar_arrive_remote(there + 8u * (uint32_t)(i % kS));
-                __syncwarp();
-            }
-    } else if (warp == 1) {
+    } else if (warp == 1 && rank == 0) {
         // --------------------------------------------------------------- MMAs
         int i = 0, it = 0;
         bool ok = true;
@@ -226,18 +209,14 @@ mx4_pair_kernel(const __grid_constant__ PairArgs a) {
             const uint32_t d = tmem + (it & 1 ? C::kD1 : 0u);
             for (int kt = 0; kt < a.KT; ++kt, ++i) {
                 const int st = i % kS;
-                // the stage is in both CTAs' shared memory, and the MMAs that
-                // read this half of the scale columns are done
-                ok = mbar_wait_abortable(full + st, (uint32_t)(i / kS) & 1u, flags) &&
-                     mbar_wait_cluster_abortable(peer + st, (uint32_t)(i / kS) & 1u, flags) &&
-                     (i < 2 || mbar_wait_abortable(empty + (i - 2) % kS, (uint32_t)((i - 2) / kS) & 1u, flags));
+                ok = mbar_wait_abortable(full + st, (uint32_t)(i / kS) & 1u, flags);   // in both CTAs
                 if (!(ok = __all_sync(0xFFFFFFFFu, ok))) break;
                 tc_fence_after();
                 const int64_t left = a.K - (int64_t)kt * kTileK;
                 if (elect_one()) {
                     const uint32_t sA = smem_u32(smem + st * C::kStage), sB = sA + C::kA, sfA = sB + C::kB,
                                    sfB = sfA + C::kSfA;
-                    const uint32_t tA = tmem + C::kSf + (uint32_t)(i & 1) * C::kSfCols, tB = tA + 8;
+                    const uint32_t tA = tmem + C::kSf + (uint32_t)st * C::kSfCols, tB = tA + 8;
                     const uint64_t ad = smem_desc_sw128(sA), bd = smem_desc_sw128(sB);
                     const int steps = left >= kTileK ? 4 : (int)((left + 63) / 64);
                     // scales: four columns per 128 rows and group
@@ -261,7 +240,7 @@ mx4_pair_kernel(const __grid_constant__ PairArgs a) {
                 __syncwarp();
             }
         }
-    } else {
+    } else if (warp >= kEpiW0) {
         // ------------------------------------------------------------ epilogue
         const int q = warp & 3;                                      // TMEM lane quarter
         uint8_t *mystg = stg + (warp - kEpiW0) * 2 * C::kStg;
@@ -275,20 +254,24 @@ mx4_pair_kernel(const __grid_constant__ PairArgs a) {
             const uint32_t d = tmem + (it & 1 ? C::kD1 : 0u) + ((uint32_t)(32 * q) << 16);
             const int arow = ta * 256 + rank * 128 + 32 * q;         // first row of A of this warp
             // the columns shared with the other accumulator first
-            constexpr int kPieces = BN / 64;
-            const int first = C::kLag == 1 && (it & 1) == 0 ? kPieces - 1 : 0;
+            constexpr int kChunks = BN / 128;
+            const int first = C::kLag == 1 && (it & 1) == 0 ? kChunks - 1 : 0;
 #pragma unroll 1
-            for (int p = 0; p < kPieces; ++p) {
-                const int c = 64 * ((p + first) % kPieces);
-                uint32_t v[64];
-                tmem_ld32(d + c, v);
-                tmem_ld32(d + c + 32, v + 32);
+            for (int p = 0; p < kChunks; ++p) {
+                const int c128 = 128 * ((p + first) % kChunks);
+                uint32_t v128[128];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) tmem_ld32(d + c128 + 32 * e, v128 + 32 * e);
                 tmem_ld_wait();
-                if (p == (C::kLag == 1 ? 0 : kPieces - 1)) {
+                if (p == (C::kLag == 1 ? 0 : kChunks - 1)) {
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive_remote(free0 + 8u * (uint32_t)(it & 1));
                 }
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {
+                const uint32_t *v = v128 + 64 * hf;
+                const int c = c128 + 64 * hf;
                 if constexpr (SLICES) {
                     const int64_t n = arow + lane;
                     const int m0 = (tb * BN + c) / kMxSlices;
@@ -334,6 +317,7 @@ mx4_pair_kernel(const __grid_constant__ PairArgs a) {
                         ++piece;
                     }
                 }
+                }
             }
         }
         if (lane == 0) bulk_wait_all();                              // Y is written before the CTA ends
@@ -344,8 +328,10 @@ mx4_pair_kernel(const __grid_constant__ PairArgs a) {
     __syncthreads();
     if (threadIdx.x == 0 && flags[0]) {
         atomicOr(&g_pair_timeout, 1u);
-        for (int s = 0; s < kS && s < flags[1]; ++s)
-            mbar_wait_bounded(full + s, (uint32_t)((flags[1] - 1 - s) / kS) & 1u);
+        // a pair's stage may stay incomplete once one of its CTAs gave up, so
+        // loads are given a millisecond (a load takes microseconds) to land
+        const uint64_t t0 = global_ns();
+        while (global_ns() - t0 < 1000000ull) __nanosleep(1000);
         for (int s = 0; s < kS && s < flags[2]; ++s)
             mbar_wait_bounded(empty + s, (uint32_t)((flags[2] - 1 - s) / kS) & 1u);
     }
@@ -391,28 +377,25 @@ mq_status launch_mx_pair(const MxProduct &p, cudaStream_t st) {
     cudaError_t e = slices ? pick<BN, true>(&fn, &smem) : pick<BN, false>(&fn, &smem);
     if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
     PairArgs a{};
-    a.as = slices ? w->scales : p.xscales;
-    a.bs = slices ? p.xscales : w->scales;
     a.Y = p.Y;
     a.ldy = p.ldy;
     a.M = (int)p.M;
     a.N = (int)w->rows;
     a.K = w->K;
-    a.G = mx_groups(w->K);
     a.KT = (int)((w->K + kTileK - 1) / kTileK);
     a.out = p.out;
     const int64_t Ta = (ra + 255) / 256, Tb = (rb + BN - 1) / BN;
     if (Ta * Tb > 0x3FFFFFFF) return fail(MQ_ERR_UNSUPPORTED, "too many output tiles");
     a.Ta = (int)Ta;
     a.Tb = (int)Tb;
-    a.a_bands = (ra + 127) / 128;
-    a.b_bands = (rb + 127) / 128;
     // TMA stores want row strides in 16 bytes, and cut a box off at the tensor's
     // edge in steps of 16 bytes only (columns behind an odd N were overwritten)
     const int size = p.out == MQ_F32 ? 4 : 2;
     a.tma_y = !slices && p.ldy * size % 16 == 0 && w->rows * size % 16 == 0;
     if (!mx_encode_codes(&a.amap, slices ? w->codes : p.xcodes, ra, w->K, 128) ||
         !mx_encode_codes(&a.bmap, slices ? p.xcodes : w->codes, rb, w->K, BN / 2) ||
+        !mx_encode_scales(&a.asmap, slices ? w->scales : p.xscales, ra, w->K, 1) ||
+        !mx_encode_scales(&a.bsmap, slices ? p.xscales : w->scales, rb, w->K, BN / 128) ||
         (a.tma_y && !mx_encode_y(&a.ymap, p.Y, p.M, w->rows, p.ldy, p.out)))
         return fail(MQ_ERR_CUDA, "cuTensorMapEncodeTiled (MXFP4 product)");
     int64_t clusters = Ta * Tb < 74 ? Ta * Tb : 74;

@@ -395,6 +395,15 @@ __device__ __forceinline__ void mma_commit_pair(uint64_t *bar) {
         ::"r"(smem_u32(bar)), "h"((uint16_t)3) : "memory");
 }
 
+// tma_load_2d whose bytes complete on a barrier of either CTA of the pair
+// (`bar`: its shared::cluster address); the box lands in this CTA.
+__device__ __forceinline__ void tma_load_2d_pair(void *dst, const void *map, int x, int y, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+        " [%0], [%1, {%2, %3}], [%4];"
+        ::"r"(smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(bar) : "memory");
+}
+
 // Tiled 2-D tensor store (TMA) of one box from shared memory, in this thread's
 // bulk group; parts of the box beyond the tensor are not written.
 __device__ __forceinline__ void tma_store_2d(const void *map, int x, int y, const void *src) {
