@@ -9,65 +9,91 @@
 namespace mq {
 namespace {
 
-// Eight consecutive elements as fp32.
+// Two fp32 numbers in one 64-bit register pair (one instruction for both).
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float &a, float &b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+// Eight numbers times f to eight codes.
+__device__ __forceinline__ uint32_t scaled_codes8(const float (&u)[8], float f) {
+    const uint64_t ff = pair(f, f);
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) unpair(mul2(pair(u[2 * i], u[2 * i + 1]), ff), v[2 * i], v[2 * i + 1]);
+    return mx_codes8(v);
+}
+
+// Eight consecutive elements as loaded: one or two 16-byte words.  amax is the
+// largest magnitude of the block of 32 in this and the three adjacent lanes, as
+// fp32 bits; magnitudes are compared as integers, so that a NaN wins.
 template <int DT>
-struct Raw8;                                  // as loaded: one or two 16-byte words
-template <>
-struct Raw8<MQ_BF16> {
+struct Raw8 {
     uint4 v;
+    static constexpr int kBytes = 2;
     __device__ void load(const void *p) { v = __ldcs(reinterpret_cast<const uint4 *>(p)); }
     __device__ void zero() { v = make_uint4(0u, 0u, 0u, 0u); }
+    __device__ uint32_t amax() const {
+        constexpr uint32_t kMag = 0x7FFF7FFFu;
+        uint32_t m = __vmaxu2(__vmaxu2(v.x & kMag, v.y & kMag), __vmaxu2(v.z & kMag, v.w & kMag));
+        m = __vmaxu2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+        m = __vmaxu2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+        m = max(m & 0xFFFFu, m >> 16);
+        if constexpr (DT == MQ_BF16) return m << 16;
+        return __float_as_uint(__half2float(__ushort_as_half((unsigned short)m))) & 0x7FFFFFFFu;
+    }
     __device__ void get(float (&f)[8]) const {
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            f[2 * i] = __uint_as_float(w[i] << 16);
-            f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+            if constexpr (DT == MQ_BF16) {
+                f[2 * i] = __uint_as_float(w[i] << 16);
+                f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+            } else {
+                const float2 t = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
+                f[2 * i] = t.x;
+                f[2 * i + 1] = t.y;
+            }
         }
     }
-    static constexpr int kBytes = 2;
-};
-template <>
-struct Raw8<MQ_F16> {
-    uint4 v;
-    __device__ void load(const void *p) { v = __ldcs(reinterpret_cast<const uint4 *>(p)); }
-    __device__ void zero() { v = make_uint4(0u, 0u, 0u, 0u); }
-    __device__ void get(float (&f)[8]) const {
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 t = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
-            f[2 * i] = t.x;
-            f[2 * i + 1] = t.y;
-        }
-    }
-    static constexpr int kBytes = 2;
 };
 template <>
 struct Raw8<MQ_F32> {
     uint4 a, b;
+    static constexpr int kBytes = 4;
     __device__ void load(const void *p) {
         a = __ldcs(reinterpret_cast<const uint4 *>(p));
         b = __ldcs(reinterpret_cast<const uint4 *>(p) + 1);
     }
     __device__ void zero() { a = b = make_uint4(0u, 0u, 0u, 0u); }
+    __device__ uint32_t amax() const {
+        const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = max(m, w[i] & 0x7FFFFFFFu);
+        m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+        return max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+    }
     __device__ void get(float (&f)[8]) const {
         const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
         for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(w[i]);
     }
-    static constexpr int kBytes = 4;
 };
-
-// Largest magnitude (as bits, so that a NaN wins) of a block of 32: eight
-// numbers in each of four adjacent lanes.
-__device__ __forceinline__ uint32_t block_amax(const float (&f)[8]) {
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(f[i]) & 0x7FFFFFFFu);
-    m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-    return max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-}
 
 // The four scale bytes of 128 columns (16 lanes), gathered in each lane.
 __device__ __forceinline__ uint32_t gather_scales(uint32_t E, int lane) {
@@ -76,43 +102,42 @@ __device__ __forceinline__ uint32_t gather_scales(uint32_t E, int lane) {
     return w | __shfl_xor_sync(0xFFFFFFFFu, w, 8);
 }
 
-constexpr int kQRows = 4;                     // rows per warp and step (loads in flight)
+// Rows per warp and step: so many 16-byte loads of a thread are in flight.
+__host__ __device__ constexpr int quant_rows(int dtype) { return dtype == MQ_F32 ? 4 : 8; }
+constexpr int kDeqRows = 8;
 
-// One warp: 256 columns of four rows.  Steps beyond the matrix (the padding
-// rows and columns of the scale blocks) write zero scale bytes only.
+// One warp: 256 columns of a few rows (all in one 128-row band).  Steps beyond
+// the matrix (the padding rows and columns of the scale blocks) write zero scale
+// bytes only.
 template <int DT>
 __global__ void __launch_bounds__(256)
 mx_quantize_kernel(const uint8_t *__restrict__ X, int64_t rows, int64_t K, int64_t ld_bytes,
                    uint8_t *__restrict__ codes, uint8_t *__restrict__ scales) {
+    constexpr int kRows = quant_rows(DT);
     const int lane = threadIdx.x & 31;
-    const int64_t G = mx_groups(K), C = (K + 255) / 256, quads = (rows + 127) / 128 * (128 / kQRows);
-    const int64_t total = quads * C, nwarps = ((int64_t)gridDim.x * blockDim.x) >> 5;
+    const int64_t G = mx_groups(K), C = (K + 255) / 256, steps = (rows + 127) / 128 * (128 / kRows);
+    const int64_t total = steps * C, nwarps = ((int64_t)gridDim.x * blockDim.x) >> 5;
     for (int64_t i = (blockIdx.x * (int64_t)blockDim.x + threadIdx.x) >> 5; i < total; i += nwarps) {
-        const int64_t r0 = i / C * kQRows, c = (i % C) * 256 + lane * 8;
-        Raw8<DT> raw[kQRows];
+        const int64_t r0 = i / C * kRows, c = (i % C) * 256 + lane * 8;
+        const int live = c < K ? (int)(rows - r0 < kRows ? (rows > r0 ? rows - r0 : 0) : kRows) : 0;
+        const uint8_t *src = X + r0 * ld_bytes + c * Raw8<DT>::kBytes;
+        Raw8<DT> raw[kRows];
 #pragma unroll
-        for (int j = 0; j < kQRows; ++j) {
-            if (r0 + j < rows && c < K) raw[j].load(X + (r0 + j) * ld_bytes + c * Raw8<DT>::kBytes);
+        for (int j = 0; j < kRows; ++j) {
+            if (j < live) raw[j].load(src + j * ld_bytes);
             else raw[j].zero();
         }
+        uint8_t *dst = codes + r0 * (K / 2) + c / 2;
+        uint8_t *sc = scales + mx_scale_at(r0, c >> 7, G) + ((lane >> 2) & 3);   // 16 bytes a row
+        const bool write_scale = (lane & 3) == 0 && c < G * 128;
 #pragma unroll
-        for (int j = 0; j < kQRows; ++j) {
-            const int64_t row = r0 + j;
-            float f[8];
-            raw[j].get(f);
-            const uint32_t E = mx_scale_byte(block_amax(f));
-            const uint32_t sw = gather_scales(E, lane);
-            if ((lane & 15) == 0 && c < G * 128)
-                *reinterpret_cast<uint32_t *>(scales + mx_scale_at(row, c >> 7, G)) = sw;
-            if (row < rows && c < K) {
-                uint32_t code = 0;
-                if (E != 255u) {
-                    const float inv = mx_inverse(E);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) f[e] *= inv;
-                    code = mx_codes8(f);
-                }
-                *reinterpret_cast<uint32_t *>(codes + row * (K / 2) + c / 2) = code;
+        for (int j = 0; j < kRows; ++j) {
+            const uint32_t E = mx_scale_byte(raw[j].amax());
+            if (write_scale) sc[j * 16] = (uint8_t)E;
+            if (j < live) {
+                float f[8];
+                raw[j].get(f);
+                *reinterpret_cast<uint32_t *>(dst + j * (K / 2)) = E == 255u ? 0u : scaled_codes8(f, mx_inverse(E));
             }
         }
     }
@@ -134,7 +159,7 @@ mx_slices_kernel(const uint8_t *__restrict__ X, int64_t M, int64_t K, int64_t ld
         else raw.zero();
         float u[8];
         raw.get(u);
-        uint32_t E = mx_slice0_byte(block_amax(u));
+        uint32_t E = mx_slice0_byte(raw.amax());
         const bool bad = E == 255u;
         const float inv = bad ? 0.f : mx_inverse(E);
 #pragma unroll
@@ -153,37 +178,41 @@ mx_slices_kernel(const uint8_t *__restrict__ X, int64_t M, int64_t K, int64_t ld
     }
 }
 
-// One warp: 256 columns of four rows.
+// One warp: 256 columns of a few rows.
 template <bool F32>
 __global__ void __launch_bounds__(256)
 mx_dequantize_kernel(const uint8_t *__restrict__ codes, const uint8_t *__restrict__ scales, int64_t rows,
                      int64_t K, uint8_t *__restrict__ out, int64_t ld_bytes) {
     const int lane = threadIdx.x & 31;
-    const int64_t G = mx_groups(K), C = (K + 255) / 256, quads = (rows + kQRows - 1) / kQRows;
-    const int64_t total = quads * C, nwarps = ((int64_t)gridDim.x * blockDim.x) >> 5;
+    const int64_t G = mx_groups(K), C = (K + 255) / 256, steps = (rows + kDeqRows - 1) / kDeqRows;
+    const int64_t total = steps * C, nwarps = ((int64_t)gridDim.x * blockDim.x) >> 5;
     for (int64_t i = (blockIdx.x * (int64_t)blockDim.x + threadIdx.x) >> 5; i < total; i += nwarps) {
-        const int64_t r0 = i / C * kQRows, c = (i % C) * 256 + lane * 8;
+        const int64_t r0 = i / C * kDeqRows, c = (i % C) * 256 + lane * 8;
         if (c >= K) continue;
-        uint32_t w[kQRows], E[kQRows];
+        const int live = rows - r0 < kDeqRows ? (int)(rows - r0) : kDeqRows;
+        const uint8_t *src = codes + r0 * (K / 2) + c / 2;
+        const uint8_t *sc = scales + mx_scale_at(r0, c >> 7, G) + ((c >> 5) & 3);
+        uint8_t *dst = out + r0 * ld_bytes + c * (F32 ? 4 : 2);
+        uint32_t w[kDeqRows], E[kDeqRows];
 #pragma unroll
-        for (int j = 0; j < kQRows; ++j) {
+        for (int j = 0; j < kDeqRows; ++j) {
             w[j] = E[j] = 0;
-            if (r0 + j < rows) {
-                w[j] = __ldcs(reinterpret_cast<const uint32_t *>(codes + (r0 + j) * (K / 2) + c / 2));
-                E[j] = scales[mx_scale_at(r0 + j, c >> 7, G) + ((c >> 5) & 3)];
+            if (j < live) {
+                w[j] = __ldcs(reinterpret_cast<const uint32_t *>(src + j * (K / 2)));
+                E[j] = sc[j * 16];
             }
         }
 #pragma unroll
-        for (int j = 0; j < kQRows; ++j) {
-            if (r0 + j >= rows) break;
+        for (int j = 0; j < kDeqRows; ++j) {
+            if (j >= live) break;
             float u[8];
             mx_units8(w[j], u);
-            const float s = mx_value(E[j]);
+            const uint64_t s2 = pair(mx_value(E[j]), mx_value(E[j]));
 #pragma unroll
-            for (int e = 0; e < 8; ++e) u[e] *= s;              // exact (at most 2 significant bits)
-            uint8_t *p = out + (r0 + j) * ld_bytes;
+            for (int e = 0; e < 4; ++e)                             // exact (at most 2 significant bits)
+                unpair(mul2(pair(u[2 * e], u[2 * e + 1]), s2), u[2 * e], u[2 * e + 1]);
             if constexpr (F32) {
-                float4 *q = reinterpret_cast<float4 *>(p + c * 4);
+                float4 *q = reinterpret_cast<float4 *>(dst + j * ld_bytes);
                 q[0] = make_float4(u[0], u[1], u[2], u[3]);
                 q[1] = make_float4(u[4], u[5], u[6], u[7]);
             } else {
@@ -193,7 +222,7 @@ mx_dequantize_kernel(const uint8_t *__restrict__ codes, const uint8_t *__restric
                     const __nv_bfloat162 b = __floats2bfloat162_rn(u[2 * e], u[2 * e + 1]);
                     h[e] = *reinterpret_cast<const uint32_t *>(&b);
                 }
-                *reinterpret_cast<uint4 *>(p + c * 2) = make_uint4(h[0], h[1], h[2], h[3]);
+                *reinterpret_cast<uint4 *>(dst + j * ld_bytes) = make_uint4(h[0], h[1], h[2], h[3]);
             }
         }
     }
@@ -208,68 +237,86 @@ __device__ __forceinline__ float scaled_level_odd(double s, double u, double z) 
     return (double)f == w ? f : __uint_as_float(__float_as_uint(f) | 1u);
 }
 
-// One thread: 32 columns of a row (one word of each plane), which are one
-// block of MXFP4; four adjacent lanes hold a row's 128 columns, so a warp
-// reads 128 contiguous bytes of each plane and writes whole 64-byte runs.
+// The block (32 columns of a row, one word of each plane) as MXFP4: returns the
+// scale byte, codes in c.
+template <int R>
+__device__ __forceinline__ uint32_t nested_block(const uint32_t (&P)[8], float s, float z, uint32_t (&c)[4]) {
+    constexpr float kHalf = R == 8 ? 0.5f : (float)(1 << (7 - R > 0 ? 7 - R : 0));   // 2^(7-r)
+    uint32_t B[8];
+    byte_words<R>(P, B);                                             // byte b of B[e]: column 8 b + e
+    float v[4][8];
+    uint32_t E;
+    float f;
+    if (z >= 32.f && z < 4096.f) {
+        // The level minus z has at most 13 significant bits here, so its product
+        // with the 11 bits of s is exact in fp32, and so is every step: a byte
+        // is set into 2^15 + byte by one permute, the rest is one addition and,
+        // once the block's largest level is known, one multiplication by s
+        // times the power of two.
+        const uint64_t off = pair(kHalf - z - 32768.f, kHalf - z - 32768.f);
+        float m = 0.f;
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+#pragma unroll
+            for (int e = 0; e < 8; e += 2) {
+                const uint32_t sel = 0x7604u | ((uint32_t)b << 4);
+                const uint64_t t = add2(pair(__uint_as_float(prmt(B[e], 0x47000000u, sel)),
+                                             __uint_as_float(prmt(B[e + 1], 0x47000000u, sel))), off);
+                unpair(t, v[b][e], v[b][e + 1]);
+                m = fmaxf(m, fmaxf(fabsf(v[b][e]), fabsf(v[b][e + 1])));
+            }
+        const float a = s * m;
+        E = mx_scale_byte(__float_as_uint(a));
+        f = a > 0.f ? s * mx_inverse(E) : s;                         // all zeros: keep their signs
+    } else {
+        // other zero points (none in practice): 64 bits, cut with a sticky bit
+        uint32_t m = 0;
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                v[b][e] = scaled_level_odd(s, (double)((B[e] >> (8 * b)) & 0xFFu) + (double)kHalf, z);
+                m = max(m, __float_as_uint(v[b][e]) & 0x7FFFFFFFu);
+            }
+        E = mx_scale_byte(m);
+        f = E == 255u ? 0.f : mx_inverse(E);
+    }
+#pragma unroll
+    for (int b = 0; b < 4; ++b) c[b] = E == 255u ? 0u : scaled_codes8(v[b], f);
+    return E;
+}
+
+// One thread: one word of each plane, which is one block of MXFP4; four adjacent
+// lanes hold a row's 128 columns, so a warp reads 128 contiguous bytes of each
+// plane and writes whole 64-byte runs.  A block of threads takes whole 128 x 128
+// blocks, so nothing is divided per thread.
 template <int R>
 __global__ void __launch_bounds__(256)
 mx_from_nested_kernel(const uint32_t *__restrict__ planes, const uint16_t *__restrict__ s16,
                       const uint16_t *__restrict__ z16, int64_t N, int64_t K,
                       uint8_t *__restrict__ codes, uint8_t *__restrict__ scales) {
-    const int64_t G = K / kGroup, N128 = (N + 127) / 128 * 128;
-    const int64_t plane_words = N128 * (K / 32);
-    const int lane = threadIdx.x & 31;
-    constexpr float kHalf = R == 8 ? 0.5f : (float)(1 << (7 - R > 0 ? 7 - R : 0));   // 2^(7-r)
-    for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < plane_words;
-         i += (int64_t)gridDim.x * blockDim.x) {
-        const int64_t block = i >> 9;                            // (row tile, group)
-        const int w = (int)(i & 3), n = (int)(i >> 2) & 127;     // word and row of the block
-        const int64_t t = block / G, g = block - t * G, row = t * 128 + n;
-        uint32_t P[8], B[8];
+    const int64_t G = K / kGroup, blocks = (N + 127) / 128 * G, plane_words = blocks * 512;
+    const int w = threadIdx.x & 3, n0 = (int)(threadIdx.x >> 2);     // word and first row of this thread
+    for (int64_t block = blockIdx.x; block < blocks; block += gridDim.x) {
+        const int64_t t = block / G, g = block - t * G;
+        uint32_t P[2][8];
+        float s[2], z[2];
 #pragma unroll
-        for (int p = 0; p < 8; ++p) P[p] = p < R ? __ldcs(planes + p * plane_words + i) : 0u;
-        const float s = __half2float(__ushort_as_half(s16[block * 128 + n]));
-        const float z = z16 ? __half2float(__ushort_as_half(z16[block * 128 + n])) : 128.f;
-        byte_words<R>(P, B);                                     // byte b of B[e]: column 8 b + e
-        float v[4][8];
-        // For 32 <= z < 4096 the level minus z has at most 13 significant
-        // bits, so its product with the 11 bits of s is exact in fp32; other
-        // zero points (none in practice) take the 64-bit form.
-        if (z >= 32.f && z < 4096.f) {
-            const float off = kHalf - z;
+        for (int h = 0; h < 2; ++h) {
 #pragma unroll
-            for (int b = 0; b < 4; ++b)
-#pragma unroll
-                for (int e = 0; e < 8; ++e) v[b][e] = s * ((float)((B[e] >> (8 * b)) & 0xFFu) + off);
-        } else {
-#pragma unroll
-            for (int b = 0; b < 4; ++b)
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    v[b][e] = scaled_level_odd(s, (double)((B[e] >> (8 * b)) & 0xFFu) + (double)kHalf, z);
+            for (int p = 0; p < 8; ++p)
+                P[h][p] = p < R ? __ldcs(planes + p * plane_words + block * 512 + h * 256 + threadIdx.x) : 0u;
+            s[h] = __half2float(__ushort_as_half(s16[block * 128 + h * 64 + n0]));
+            z[h] = z16 ? __half2float(__ushort_as_half(z16[block * 128 + h * 64 + n0])) : 128.f;
         }
-        uint32_t m = 0;
 #pragma unroll
-        for (int b = 0; b < 4; ++b)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(v[b][e]) & 0x7FFFFFFFu);
-        const uint32_t E = row < N ? mx_scale_byte(m) : 0u;
-        uint32_t sw = E << (8 * w);
-        sw |= __shfl_xor_sync(0xFFFFFFFFu, sw, 1);
-        sw |= __shfl_xor_sync(0xFFFFFFFFu, sw, 2);
-        if ((lane & 3) == 0) *reinterpret_cast<uint32_t *>(scales + mx_scale_at(row, g, G)) = sw;
-        if (row < N) {
-            uint32_t c[4] = {0, 0, 0, 0};
-            if (E != 255u) {
-                const float inv = mx_inverse(E);
-#pragma unroll
-                for (int b = 0; b < 4; ++b) {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) v[b][e] *= inv;
-                    c[b] = mx_codes8(v[b]);
-                }
-            }
-            *reinterpret_cast<uint4 *>(codes + row * (K / 2) + g * 64 + w * 16) = make_uint4(c[0], c[1], c[2], c[3]);
+        for (int h = 0; h < 2; ++h) {
+            const int64_t row = t * 128 + h * 64 + n0;
+            uint32_t c[4];
+            const uint32_t E = nested_block<R>(P[h], s[h], z[h], c);
+            scales[mx_scale_at(row, g, G) + w] = (uint8_t)(row < N ? E : 0u);
+            if (row < N)
+                *reinterpret_cast<uint4 *>(codes + row * (K / 2) + g * 64 + w * 16) = make_uint4(c[0], c[1], c[2], c[3]);
         }
     }
 }
@@ -341,7 +388,7 @@ extern "C" mq_status mq_mx4_quantize(const void *X, int dtype, int64_t rows, int
     cudaStream_t st = (cudaStream_t)stream;
     const mq_status bs = bind_device(st);
     if (bs != MQ_OK) return bs;
-    const int grid = grid_for((rows + 127) / 128 * (128 / kQRows) * ((K + 255) / 256) * 32, 256);
+    const int grid = grid_for((rows + 127) / 128 * (128 / quant_rows(dtype)) * ((K + 255) / 256) * 32, 256);
     const uint8_t *x = static_cast<const uint8_t *>(X);
     if (dtype == MQ_BF16)
         mx_quantize_kernel<MQ_BF16><<<grid, 256, 0, st>>>(x, rows, K, ld * size, codes_out, scales_out);
@@ -368,7 +415,7 @@ extern "C" mq_status mq_mx4_from_nested(const mq_weights *w, uint8_t *codes_out,
     static const Fn fns[8] = {mx_from_nested_kernel<1>, mx_from_nested_kernel<2>, mx_from_nested_kernel<3>,
                               mx_from_nested_kernel<4>, mx_from_nested_kernel<5>, mx_from_nested_kernel<6>,
                               mx_from_nested_kernel<7>, mx_from_nested_kernel<8>};
-    const int grid = grid_for((w->N + 127) / 128 * 128 * (w->K / 32), 256);
+    const int grid = grid_for((w->N + 127) / 128 * (w->K / kGroup), 1);
     fns[w->r - 1]<<<grid, 256, 0, st>>>(w->planes, w->scales, w->zeros, w->N, w->K, codes_out, scales_out);
     const cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? MQ_OK : cuda_fail(e, "mx_from_nested_kernel");
@@ -387,7 +434,7 @@ extern "C" mq_status mq_mx4_dequantize(const mq_mx4 *m, void *out, int dtype, in
         return fail(MQ_ERR_MISALIGNED, "mq_mx4_dequantize: out and its row stride must be 16-byte aligned");
     cudaStream_t st = (cudaStream_t)stream;
     if ((s = bind_device(st)) != MQ_OK) return s;
-    const int grid = grid_for((m->rows + kQRows - 1) / kQRows * ((m->K + 255) / 256) * 32, 256);
+    const int grid = grid_for((m->rows + kDeqRows - 1) / kDeqRows * ((m->K + 255) / 256) * 32, 256);
     uint8_t *o = static_cast<uint8_t *>(out);
     if (dtype == MQ_F32)
         mx_dequantize_kernel<true><<<grid, 256, 0, st>>>(m->codes, m->scales, m->rows, m->K, o, ld * size);

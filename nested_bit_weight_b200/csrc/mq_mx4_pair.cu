@@ -203,7 +203,7 @@ mx4_pair_kernel(const __grid_constant__ PairArgs a) {
         for (int tile = cluster; tile < tiles && ok; tile += nclusters, ++it) {
             if (it >= C::kLag) {
                 const int w = it - C::kLag;
-                ok = mbar_wait_cluster_abortable(dfree + (w & 1), (uint32_t)(w >> 1) & 1u, flags);
+                ok = mbar_wait_abortable(dfree + (w & 1), (uint32_t)(w >> 1) & 1u, flags);
                 if (!(ok = __all_sync(0xFFFFFFFFu, ok))) break;
             }
             const uint32_t d = tmem + (it & 1 ? C::kD1 : 0u);
@@ -266,7 +266,7 @@ mx4_pair_kernel(const __grid_constant__ PairArgs a) {
                 if (p == (C::kLag == 1 ? 0 : kChunks - 1)) {
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive_remote(free0 + 8u * (uint32_t)(it & 1));
+                    if (lane == 0) mbar_arrive_remote_weak(free0 + 8u * (uint32_t)(it & 1));
                 }
 #pragma unroll
                 for (int hf = 0; hf < 2; ++hf) {

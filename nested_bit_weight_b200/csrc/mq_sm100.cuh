@@ -502,6 +502,12 @@ __device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];"
                  ::"r"(cluster_addr) : "memory");
 }
+// The same with the default (CTA-scope) release: for hand-offs that carry no
+// memory writes, such as tensor memory read (the cluster-scope release costs
+// about as much as a tile of the smallest MMAs).
+__device__ __forceinline__ void mbar_arrive_remote_weak(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
 // try_wait with cluster-scope acquire (for parts written by other CTAs).
 __device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t *bar, uint32_t parity) {
     uint32_t ok;
