@@ -35,6 +35,8 @@ struct MxProduct {
     void *Y;
     int out;
     int64_t ldy;
+    const uint16_t *X;             // bf16 rows cut within the product (few rows), or NULL
+    int64_t ldx;
 };
 bool mx_pair_takes(const MxProduct &p);
 mq_status launch_mx_pair(const MxProduct &p, cudaStream_t st);

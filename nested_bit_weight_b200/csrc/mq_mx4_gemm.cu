@@ -11,13 +11,20 @@
 //
 // Work: one cluster of CS CTAs per output tile, each CTA a contiguous share of
 // K; the parts are summed through distributed shared memory, in CTA order
-// (deterministic, no workspace).
+// (deterministic, no workspace): each CTA writes its part of a column to the
+// CTA that owns the column, which adds what it was sent.
 //
-// Roles: a warp whose one thread loads (TMA for the codes, one bulk copy per
-// row band for the scales), a warp whose one thread copies the scales to TMEM
-// and issues the MMAs, four warps for the epilogue.  Scales have their own
-// TMEM columns for each stage of the shared-memory ring, so a stage's scales
-// are overwritten only once its MMAs are done.
+// Roles: a warp that loads (TMA for the codes, bulk copies for the scales), a
+// warp that copies the scales to TMEM and issues the MMAs, four warps for the
+// epilogue.  With one or two bf16 rows (FUSED) those four make the eight MXFP4
+// rows of each row themselves, a stage at a time, straight into the MMA's
+// operand; every CTA repeats that small work, and a launch and a pass through
+// memory are saved.  Scales have their own TMEM columns for each stage of the
+// shared-memory ring, so a stage's scales are overwritten only once its MMAs
+// are done.
+//
+// Programmatic dependent launch: nothing is read or written before
+// griddepcontrol.wait; the weights are only brought into L2 before it.
 //
 // Every wait is bounded (about a second); one that gives up sets a CTA abort
 // flag and the device flag read by mq_device_status.  Copies and MMAs in
@@ -37,6 +44,10 @@ namespace {
 
 using namespace sm100;
 
+#ifndef MX_FILL2
+#define MX_FILL2 296
+#define MX_FILL1 148
+#endif
 constexpr int kTileN = 128;                  // weight rows per tile (MMA M)
 constexpr int kTileK = 256;                  // columns per stage (128 bytes of codes a row)
 constexpr int kThreads = 192;
@@ -64,34 +75,84 @@ struct MxCfg {
     static constexpr uint32_t kCols = kSf + kStages * kSfCols <= 256 ? 256 : 512;
     static_assert(kSf + kStages * kSfCols <= kCols, "TMEM columns");
     static constexpr size_t kSmem = 1024 + (size_t)kStages * kStage + 1024;
-    // the parts of a split tile lie in the ring: 128 x BN fp32
-    static_assert((size_t)kStages * kStage >= (size_t)BN * kTileN * 4, "parts fit the ring");
+    // the parts sent to a CTA lie in the ring: at most 128 x (BN + 8) fp32
+    static_assert((size_t)kStages * kStage >= (size_t)(BN + 8) * kTileN * 4, "parts fit the ring");
 };
 
 struct MxArgs {
     CUtensorMap wmap, xmap;        // codes as (K / 2 bytes, rows), boxes 128 x 128 and 128 x BN
     const uint8_t *ws, *xs;        // scales
+    const uint8_t *X;              // FUSED: bf16 rows and their stride in bytes
+    int64_t ldx_bytes;
     void *Y;
     int64_t ldy;
     int M, N;                      // rows of X before slicing, output features
     int64_t K, G;                  // columns, 128-column groups
     int MB, KT, CS;                // X tiles, K tiles, CTAs per output tile
+    int lper;                      // log2 of the columns a CTA of a cluster adds up
     int slices;                    // 1, or kMxSlices columns of D per row of X
     int out;                       // type of Y
 };
 
-__device__ __forceinline__ void store_y(const MxArgs &a, int64_t m, int64_t n, float v) {
-    const int64_t at = m * a.ldy + n;
-    if (a.out == MQ_BF16) static_cast<__nv_bfloat16 *>(a.Y)[at] = __float2bfloat16_rn(v);
-    else if (a.out == MQ_F16) static_cast<__half *>(a.Y)[at] = __float2half_rn(v);
-    else static_cast<float *>(a.Y)[at] = v;
+// Up to this many bf16 rows are cut into slices inside the product.  Cutting a
+// row is one chain of dependent operations, about 800 clocks a stage, which the
+// four warps run side by side on different stages (one row) or on two stages
+// (two rows); with eight rows it took 25 us for 14336 x 4096 where a kernel of
+// its own takes 2.
+constexpr int kFusedRows = 2;
+
+template <class T>
+__device__ __forceinline__ T to(float v);
+template <>
+__device__ __forceinline__ float to<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ __half to<__half>(float v) { return __float2half_rn(v); }
+template <>
+__device__ __forceinline__ __nv_bfloat16 to<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+
+template <class T>
+struct alignas(4 * sizeof(T)) Vec4 {
+    T v[4];
+};
+
+// Y's columns first .. first + count of this tile: the CS parts (in CTA order)
+// of [column][128 features], four features a thread, to Y.
+template <class T>
+__device__ __forceinline__ void sum_parts(const MxArgs &a, const float *part, int tid, int count, int64_t m0,
+                                          int64_t n0) {
+    const size_t stride = (size_t)kTileN << a.lper;            // floats of a part
+    const bool vec = a.ldy % 4 == 0;
+    T *const Y = static_cast<T *>(a.Y) + m0 * a.ldy + n0;
+#pragma unroll 4
+    for (int i = tid; i < count * 32; i += 128) {
+        const int col = i >> 5, r = (i & 31) * 4;
+        const float *p = part + (size_t)col * kTileN + r;
+        float4 y = *reinterpret_cast<const float4 *>(p);
+        for (int c = 1; c < a.CS; ++c) {
+            const float4 z = *reinterpret_cast<const float4 *>(p + c * stride);
+            y.x += z.x;
+            y.y += z.y;
+            y.z += z.z;
+            y.w += z.w;
+        }
+        T *const dst = Y + col * a.ldy + r;
+        const Vec4<T> v = {{to<T>(y.x), to<T>(y.y), to<T>(y.z), to<T>(y.w)}};
+        if (vec && n0 + r + 3 < a.N) {
+            *reinterpret_cast<Vec4<T> *>(dst) = v;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (n0 + r + e < a.N) dst[e] = v.v[e];
+        }
+    }
 }
 
-template <int BN>
+template <int BN, bool FUSED>
 __global__ void __launch_bounds__(kThreads)
 mx4_gemm_kernel(const __grid_constant__ MxArgs a) {
     using C = MxCfg<BN>;
     constexpr int kS = C::kStages;
+    constexpr int kPrefetch = 16;                // stages brought into L2 ahead
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + kS * C::kStage), *empty = full + kS, *done = empty + kS;
@@ -104,25 +165,19 @@ mx4_gemm_kernel(const __grid_constant__ MxArgs a) {
     const int k0 = (int)((int64_t)rank * a.KT / a.CS), k1 = (int)((int64_t)(rank + 1) * a.KT / a.CS);
 
     if (threadIdx.x == 0) {
+        for (int i = 0; i < kPrefetch && i < k1 - k0; ++i) tma_prefetch_2d(&a.wmap, (k0 + i) * 128, t * kTileN);
         for (int i = 0; i < kS; ++i) {
-            mbar_init(full + i, 1);
+            mbar_init(full + i, FUSED ? 1 + a.M : 1);   // the loads and the slicing warps
             mbar_init(empty + i, 1);
         }
         mbar_init(done, 1);
         flags[0] = flags[1] = flags[2] = 0;
         fence_mbar_init();
     }
+    __syncthreads();
     // the operands may come from the previous kernel; tensor memory is taken
     // after it too, so that it never waits for columns held here
     pdl_wait();
-    if (warp == 1) {
-        tmem_alloc(tmem_slot, C::kCols);
-        tmem_relinquish();
-    }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(tmem_slot);
 
     if (warp == 0) {
         // -------------------------------------------------------------- loads
@@ -141,18 +196,27 @@ mx4_gemm_kernel(const __grid_constant__ MxArgs a) {
             if (elect_one()) {
                 uint8_t *sA = smem + st * C::kStage, *sB = sA + C::kA, *sfA = sB + C::kB, *sfB = sfA + C::kSfA;
                 const uint32_t sfbytes = 512u * (uint32_t)(a.G - 2 * kt < 2 ? a.G - 2 * kt : 2);
-                mbar_expect_tx(full + st, C::kA + C::kB + sfbytes * (1 + bands));
+                mbar_expect_tx(full + st, C::kA + sfbytes + (FUSED ? 0u : C::kB + sfbytes * bands));
                 tma_load_2d(sA, &a.wmap, kt * 128, t * kTileN, full + st);
-                tma_load_2d(sB, &a.xmap, kt * 128, mb * BN, full + st);
                 bulk_g2s(sfA, a.ws + ((int64_t)t * a.G + 2 * kt) * 512, sfbytes, full + st);
-                for (int b = 0; b < bands; ++b)
-                    bulk_g2s(sfB + b * 1024, a.xs + ((xband + b) * a.G + 2 * kt) * 512, sfbytes, full + st);
+                if constexpr (!FUSED) {
+                    tma_load_2d(sB, &a.xmap, kt * 128, mb * BN, full + st);
+                    for (int b = 0; b < bands; ++b)
+                        bulk_g2s(sfB + b * 1024, a.xs + ((xband + b) * a.G + 2 * kt) * 512, sfbytes, full + st);
+                }
                 flags[1] = i + 1;
             }
             __syncwarp();
         }
     } else if (warp == 1) {
         // --------------------------------------------------------------- MMAs
+        tmem_alloc(tmem_slot, C::kCols);
+        tmem_relinquish();
+        // only now may the next kernel start: one that takes tensor memory before
+        // its own wait could otherwise hold the columns this one needs
+        pdl_launch_dependents();
+        named_arrive(1, 160);                    // the epilogue may read the address
+        const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(tmem_slot);
         for (int i = 0; i < k1 - k0; ++i) {
             const int st = i % kS;
             const bool ok = mbar_wait_abortable(full + st, (uint32_t)(i / kS) & 1u, flags);
@@ -188,40 +252,110 @@ mx4_gemm_kernel(const __grid_constant__ MxArgs a) {
     }
     __syncwarp();
 
+    if constexpr (FUSED) {
+        if (warp >= kEpiW0) {
+            // ------------------------------------------------------- slices of X
+            // 256 columns of a row at a time, eight a lane; the next values are
+            // loaded while the last are cut
+            const int groups = 4 / a.M;                              // stages at a time
+            const int m = (warp - kEpiW0) % a.M, grp = (warp - kEpiW0) / a.M;
+            const uint8_t *xrow = a.X + m * a.ldx_bytes + lane * 16;
+            const uint32_t swz = (uint32_t)(lane >> 2), at = (uint32_t)(lane & 3) * 4;
+            auto load = [&](int i) {
+                const int kt = k0 + i;
+                return kt < k1 && (int64_t)kt * kTileK + lane * 8 < a.K
+                           ? *reinterpret_cast<const uint4 *>(xrow + (int64_t)kt * kTileK * 2)
+                           : make_uint4(0u, 0u, 0u, 0u);
+            };
+            uint4 next = load(grp);
+            for (int i = grp; i < k1 - k0; i += groups) {
+                const int st = i % kS;
+                const uint32_t x[4] = {next.x, next.y, next.z, next.w};
+                next = load(i + groups);
+                float u[8];
+                uint32_t a2 = 0;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    u[2 * j] = __uint_as_float(x[j] << 16);
+                    u[2 * j + 1] = __uint_as_float(x[j] & 0xFFFF0000u);
+                    a2 = __vmaxu2(a2, x[j] & 0x7FFF7FFFu);
+                }
+                a2 = __vmaxu2(a2, __shfl_xor_sync(0xFFFFFFFFu, a2, 1));
+                a2 = __vmaxu2(a2, __shfl_xor_sync(0xFFFFFFFFu, a2, 2));
+                uint32_t E = mx_slice0_byte(max(a2 & 0xFFFFu, a2 >> 16) << 16);
+                const float inv = E == 255u ? 0.f : mx_inverse(E);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) u[j] = E == 255u ? 0.f : u[j] * inv;
+                const bool ok = i < kS || mbar_wait_backoff(empty + st, (uint32_t)(i / kS - 1) & 1u, flags);
+                if (!__all_sync(0xFFFFFFFFu, ok)) break;
+                // eight rows of B: one swizzle atom; eight rows of its scales
+                uint8_t *sB = smem + st * C::kStage + C::kA, *sf = sB + C::kB + C::kSfA + (lane >> 4) * 512 +
+                                                                  m * kMxSlices * 16 + ((lane >> 2) & 3);
+                sB += m * 1024 + at;
+#pragma unroll
+                for (int j = 0; j < kMxSlices; ++j) {
+                    const uint32_t En = mx_next_slice(E, j);
+                    *reinterpret_cast<uint32_t *>(sB + j * 128 + ((swz ^ (uint32_t)j) << 4)) = mx_slice_codes(u, E - En);
+                    if ((lane & 3) == 0) sf[j * 16] = (uint8_t)E;
+                    E = En;
+                }
+                fence_proxy_async_smem();                            // the tensor core reads what was written
+                __syncwarp();
+                if (lane == 0) mbar_arrive(full + st);
+            }
+            __syncwarp();
+        }
+    }
+
     // ------------------------------------------------------------ epilogue
-    bool ok = true;
     const int q = warp & 3, row = 32 * q + lane;              // TMEM lane quarter of this warp
-    const int64_t n = (int64_t)t * kTileN + row;
     const int cols = BN / a.slices;                           // rows of X of this tile
     const int64_t m0 = (int64_t)mb * cols;
-    float *part = reinterpret_cast<float *>(smem);            // [column][128], once the ring is idle
+    const int live = a.M - m0 < cols ? (int)(a.M - m0) : cols;
+    const int lper = a.lper, per = 1 << lper;                 // columns a CTA owns
+    float *part = reinterpret_cast<float *>(smem);            // [CTA][owned column][128], once the rings are idle
+    bool ok = true;
     if (warp >= kEpiW0) {
         ok = mbar_wait_backoff(done, 0, flags);
         ok = __all_sync(0xFFFFFFFFu, ok);
+    }
+    if (a.CS > 1) {
+        __syncwarp();
+        cluster_arrive();                                     // every CTA's ring is idle
+        cluster_wait();
+    }
+    if (warp >= kEpiW0) {
+        named_sync(1, 160);
         tc_fence_after();
         if (ok) {
-            const uint32_t base = tmem + C::kD + ((uint32_t)(32 * q) << 16);
+            const uint32_t base = *reinterpret_cast<volatile uint32_t *>(tmem_slot) + C::kD + ((uint32_t)(32 * q) << 16);
+            const uint32_t mine = smem_u32(part + ((size_t)rank << lper) * kTileN + row);
+            constexpr int kStep = BN < 32 ? BN : 32;
 #pragma unroll 1
-            for (int c = 0; c < BN; c += 8) {
-                if (m0 + c / a.slices >= a.M) break;
-                uint32_t v[8];
-                tmem_ld8(base + c, v);
+            for (int c = 0; c < BN; c += kStep) {
+                if (c / a.slices >= live) break;
+                uint32_t v[kStep];
+                if constexpr (kStep == 8) tmem_ld8(base + c, v);
+                else if constexpr (kStep == 16) tmem_ld16(base + c, v);
+                else tmem_ld32(base + c, v);
                 tmem_ld_wait();
-                float y[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) y[j] = __uint_as_float(v[j]);
-                int cnt = 8, col = c;
+                auto put = [&](int col, float y) {            // columns beyond live stay inside the parts
+                    if (a.CS > 1)
+                        st_cluster_f32(cluster_map(mine + (uint32_t)((col & (per - 1)) * kTileN * 4), (uint32_t)(col >> lper)), y);
+                    else
+                        part[col * kTileN + row] = y;
+                };
                 if (a.slices == kMxSlices) {                  // small slices first
-                    float s = y[7];
 #pragma unroll
-                    for (int j = 6; j >= 0; --j) s += y[j];
-                    y[0] = s;
-                    cnt = 1;
-                    col = c / kMxSlices;
-                }
-                for (int j = 0; j < cnt; ++j) {
-                    if (a.CS > 1) part[(col + j) * kTileN + row] = y[j];
-                    else if (n < a.N && m0 + col + j < a.M) store_y(a, m0 + col + j, n, y[j]);
+                    for (int e = 0; e < kStep / kMxSlices; ++e) {
+                        float s = __uint_as_float(v[kMxSlices * e + kMxSlices - 1]);
+#pragma unroll
+                        for (int j = kMxSlices - 2; j >= 0; --j) s += __uint_as_float(v[kMxSlices * e + j]);
+                        put(c / kMxSlices + e, s);
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < kStep; ++j) put(c + j, __uint_as_float(v[j]));
                 }
             }
         }
@@ -231,21 +365,17 @@ mx4_gemm_kernel(const __grid_constant__ MxArgs a) {
         __syncwarp();
         cluster_arrive();
         cluster_wait();
-        if (warp >= kEpiW0 && ok) {
-            // 32-row pieces of the tile's columns, dealt to the CTAs in turn
-            const int live = a.M - m0 < cols ? (int)(a.M - m0) : cols;
-            for (int u = rank * 4 + (warp - kEpiW0); u < live * 4; u += a.CS * 4) {
-                const int col = u >> 2, r = 32 * (u & 3) + lane;
-                const uint32_t at = smem_u32(part + col * kTileN + r);
-                float y = 0.f;
-                for (int c = 0; c < a.CS; ++c) y += ld_cluster_f32(cluster_map(at, (uint32_t)c));
-                const int64_t nn = (int64_t)t * kTileN + r;
-                if (nn < a.N) store_y(a, m0 + col, nn, y);
-            }
+    }
+    if (warp >= kEpiW0) {
+        if (a.CS == 1) named_sync(2, 128);
+        const int first = rank << lper, count = live - first < per ? live - first : per;
+        const int tid = threadIdx.x - 32 * kEpiW0;
+        const int64_t n0 = (int64_t)t * kTileN;
+        if (ok && count > 0) {
+            if (a.out == MQ_BF16) sum_parts<__nv_bfloat16>(a, part, tid, count, m0 + first, n0);
+            else if (a.out == MQ_F16) sum_parts<__half>(a, part, tid, count, m0 + first, n0);
+            else sum_parts<float>(a, part, tid, count, m0 + first, n0);
         }
-        __syncwarp();
-        cluster_arrive();                                     // no CTA leaves while its part is read
-        cluster_wait();
     }
 
     // ---- end: copies and MMAs in flight land (already so unless a wait gave up)
@@ -261,16 +391,16 @@ mx4_gemm_kernel(const __grid_constant__ MxArgs a) {
     __syncthreads();
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc(tmem, C::kCols);
+        tmem_dealloc(*reinterpret_cast<volatile uint32_t *>(tmem_slot), C::kCols);
     }
 }
 
 using MxFn = void (*)(MxArgs);
 
-template <int BN>
+template <int BN, bool FUSED>
 cudaError_t pick(MxFn *fn, size_t *smem) {
     static std::atomic<uint64_t> done{0};
-    *fn = mx4_gemm_kernel<BN>;
+    *fn = mx4_gemm_kernel<BN, FUSED>;
     *smem = MxCfg<BN>::kSmem;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -285,23 +415,25 @@ cudaError_t pick(MxFn *fn, size_t *smem) {
 mq_status launch(const MxProduct &p, cudaStream_t st) {
     if (mx_pair_takes(p)) return launch_mx_pair(p, st);
     const mq_mx4 *w = p.w;
+    const bool fused = p.X != nullptr;
     const int64_t cols = p.M * p.slices;
-    const int BN = cols <= 8 ? 8 : cols <= 16 ? 16 : cols <= 32 ? 32 : cols <= 64 ? 64 : cols <= 128 ? 128 : 256;
+    const int BN = cols <= 8 ? 8 : cols <= 16 ? 16 : cols <= 32 ? 32 : cols <= 64 ? 64 : 128;
     MxFn fn;
     size_t smem;
-    const cudaError_t pe = BN == 8    ? pick<8>(&fn, &smem)
-                           : BN == 16  ? pick<16>(&fn, &smem)
-                           : BN == 32  ? pick<32>(&fn, &smem)
-                           : BN == 64  ? pick<64>(&fn, &smem)
-                           : BN == 128 ? pick<128>(&fn, &smem)
-                                       : pick<256>(&fn, &smem);
+    const cudaError_t pe = BN == 8    ? fused ? pick<8, true>(&fn, &smem) : pick<8, false>(&fn, &smem)
+                           : BN == 16  ? fused ? pick<16, true>(&fn, &smem) : pick<16, false>(&fn, &smem)
+                           : BN == 32  ? pick<32, false>(&fn, &smem)
+                           : BN == 64  ? pick<64, false>(&fn, &smem)
+                                       : pick<128, false>(&fn, &smem);
     if (pe != cudaSuccess) return cuda_fail(pe, "cudaFuncSetAttribute");
     MxArgs a{};
     if (!mx_encode_codes(&a.wmap, w->codes, w->rows, w->K, kTileN) ||
-        !mx_encode_codes(&a.xmap, p.xcodes, cols, w->K, BN))
+        (!fused && !mx_encode_codes(&a.xmap, p.xcodes, cols, w->K, BN)))
         return fail(MQ_ERR_CUDA, "cuTensorMapEncodeTiled (MXFP4 codes)");
     a.ws = w->scales;
     a.xs = p.xscales;
+    a.X = reinterpret_cast<const uint8_t *>(p.X);
+    a.ldx_bytes = p.ldx * 2;
     a.Y = p.Y;
     a.ldy = p.ldy;
     a.M = (int)p.M;
@@ -313,10 +445,11 @@ mq_status launch(const MxProduct &p, cudaStream_t st) {
     a.slices = p.slices;
     a.out = p.out;
     const int64_t tiles = (w->rows + kTileN - 1) / kTileN * a.MB;
-    // K is split while the CTAs still fit the GPU once and each keeps two
-    // stages of K
+    // K is split while the CTAs still fit the GPU once (two an SM up to 64
+    // columns) and each keeps two stages of K
     a.CS = 1;
-    while (a.CS < 8 && tiles * a.CS * 2 <= 148 && a.KT >= a.CS * 4) a.CS *= 2;
+    while (a.CS < 8 && tiles * a.CS * 2 <= (BN <= 64 ? MX_FILL2 : MX_FILL1) && a.KT >= a.CS * 4) a.CS *= 2;
+    for (a.lper = 0; (a.CS << a.lper) < BN / p.slices;) ++a.lper;
     if (tiles * a.CS > 0x7FFFFFFF) return fail(MQ_ERR_UNSUPPORTED, "mq_mx4_gemm: too many output tiles");
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -426,12 +559,13 @@ extern "C" mq_status mq_mx4_gemm(const mq_mx4 *X, const mq_mx4 *w, void *Y, int 
     if ((s = check_y("mq_mx4_gemm", w->rows, Y, y_dtype, ldy)) != MQ_OK) return s;
     cudaStream_t st = (cudaStream_t)stream;
     if ((s = bind_device(st)) != MQ_OK) return s;
-    return launch(MxProduct{X->codes, X->scales, X->rows, 1, w, Y, y_dtype, ldy}, st);
+    return launch(MxProduct{X->codes, X->scales, X->rows, 1, w, Y, y_dtype, ldy, nullptr, 0}, st);
 }
 
 extern "C" size_t mq_mx4_gemm_bf16_workspace_bytes(int64_t M, int64_t N, int64_t K) {
     if (M < 1 || M > kMxMaxDim / kMxSlices || N < 1 || N > kMxMaxDim || K < kMxBlock || K % kMxBlock || K > kMxMaxDim)
         return 0;
+    if (M <= kFusedRows) return 0;
     return slice_code_bytes(M, K) + mq_mx4_scale_bytes(M * kMxSlices, K);
 }
 
@@ -453,9 +587,11 @@ extern "C" mq_status mq_mx4_gemm_bf16(const uint16_t *X, int64_t M, int64_t ldx,
         return fail(MQ_ERR_WORKSPACE, "workspace smaller than mq_mx4_gemm_bf16_workspace_bytes");
     cudaStream_t st = (cudaStream_t)stream;
     if ((s = bind_device(st)) != MQ_OK) return s;
+    if (M <= kFusedRows)
+        return launch(MxProduct{nullptr, nullptr, M, kMxSlices, w, Y, y_dtype, ldy, X, ldx}, st);
     uint8_t *codes = static_cast<uint8_t *>(workspace), *scales = codes + slice_code_bytes(M, w->K);
     if ((s = launch_mx_slices(X, M, w->K, ldx, codes, scales, st)) != MQ_OK) return s;
-    return launch(MxProduct{codes, scales, M, kMxSlices, w, Y, y_dtype, ldy}, st);
+    return launch(MxProduct{codes, scales, M, kMxSlices, w, Y, y_dtype, ldy, nullptr, 0}, st);
 }
 
 #ifdef MQ_TEST_HOOKS

@@ -343,6 +343,13 @@ __device__ __forceinline__ void tma_load_2d(void *dst, const void *map, int x, i
         ::"r"(smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar)) : "memory");
 }
 
+// Bring the box of a later tma_load_2d into L2 only.  L2 is where the GPU's
+// copies agree, so this may name memory that another kernel is still writing.
+__device__ __forceinline__ void tma_prefetch_2d(const void *map, int x, int y) {
+    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];"
+                 ::"l"(map), "r"(x), "r"(y) : "memory");
+}
+
 // Per-thread asynchronous copies global -> shared (4, 8 or 16 bytes, both
 // addresses aligned to the size), grouped per thread: commit closes a group,
 // wait<N> returns once at most N of this thread's newest groups are pending.
@@ -488,11 +495,6 @@ __device__ __forceinline__ uint32_t cluster_map(uint32_t local, uint32_t rank) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(local), "r"(rank));
     return r;
 }
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-    return v;
-}
 __device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
@@ -538,6 +540,10 @@ __device__ __forceinline__ void pdl_wait() {
 
 __device__ __forceinline__ void named_sync(int id, int n) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory");
+}
+
+__device__ __forceinline__ void named_arrive(int id, int n) {
+    asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(n) : "memory");
 }
 
 // Named barrier that also returns the AND of `v` over the n threads.
