@@ -11,8 +11,11 @@
 //
 // Work: one cluster of CS CTAs per output tile, each CTA a contiguous share of
 // K; the parts are summed through distributed shared memory, in CTA order
-// (deterministic, no workspace): each CTA writes its part of a column to the
-// CTA that owns the column, which adds what it was sent.
+// (deterministic, no workspace): each CTA stores its part of four columns
+// straight from registers to the CTA that owns them, and the stores complete
+// on that CTA's barrier, so that no CTA waits for another but the owner for what
+// it is sent (two cluster barriers and copies out of shared memory took 1.8 of
+// 8.8 us for one token through 14336 x 4096).
 //
 // Roles: a warp that loads (TMA for the codes, bulk copies for the scales), a
 // warp that copies the scales to TMEM and issues the MMAs, four warps for the
@@ -44,13 +47,10 @@ namespace {
 
 using namespace sm100;
 
-#ifndef MX_FILL2
-#define MX_FILL2 296
-#define MX_FILL1 148
-#endif
 constexpr int kTileN = 128;                  // weight rows per tile (MMA M)
 constexpr int kTileK = 256;                  // columns per stage (128 bytes of codes a row)
 constexpr int kThreads = 192;
+constexpr int kMinStages = 4;                // of K for each CTA of a split
 constexpr int kEpiW0 = 2;                    // first epilogue warp
 
 __device__ unsigned int g_mx_timeout;        // set when a bounded wait gave up
@@ -67,16 +67,25 @@ struct MxCfg {
     static constexpr uint32_t kA = kTileN * 128, kB = BN * 128;     // codes of a stage
     static constexpr uint32_t kSfA = 1024, kSfB = 1024 * kBands;    // scales of a stage
     static constexpr uint32_t kStage = kA + kB + kSfA + kSfB;       // a multiple of 1024
-    // two CTAs an SM up to 64 columns, one above
-    static constexpr int kStages = (int)(((BN <= 64 ? 113 : 226) * 1024 - 2048) / kStage) < 8
-                                       ? (int)(((BN <= 64 ? 113 : 226) * 1024 - 2048) / kStage) : 8;
+    // parts sent to this CTA: [CTA][owned columns / 4][128][4] fp32, at least four
+    // columns for each of eight CTAs
+    static constexpr uint32_t kParts = (BN < 32 ? 32 : BN) * kTileN * 4;
+    // two CTAs an SM up to 32 columns, one above
+    static constexpr int kPerSm = BN <= 32 ? 2 : 1;
+    static constexpr int kRoom = (kPerSm == 2 ? 113 : 226) * 1024 - 2048 - (int)kParts;
+    static constexpr int kStages = kRoom / (int)kStage < 6 ? kRoom / (int)kStage : 6;
     static constexpr uint32_t kSfCols = 8 + 8 * kBands;             // TMEM columns of a stage's scales
     static constexpr uint32_t kD = 0, kSf = BN < 32 ? 32 : BN;      // TMEM: accumulator, then scales
     static constexpr uint32_t kCols = kSf + kStages * kSfCols <= 256 ? 256 : 512;
     static_assert(kSf + kStages * kSfCols <= kCols, "TMEM columns");
-    static constexpr size_t kSmem = 1024 + (size_t)kStages * kStage + 1024;
-    // the parts sent to a CTA lie in the ring: at most 128 x (BN + 8) fp32
-    static_assert((size_t)kStages * kStage >= (size_t)(BN + 8) * kTileN * 4, "parts fit the ring");
+    // With one row of X the four slicing warps are on four stages at once: in a
+    // shorter ring one of them would wait two phases ahead of a barrier, which
+    // its parity cannot express.
+    static_assert(kStages >= 4, "ring");
+    static constexpr size_t kSmem = 1024 + (size_t)kStages * kStage + kParts + 1024;
+    // no more CTAs on an SM than tensor memory has room for: one that waited for
+    // columns could hold up the cluster that holds them
+    static_assert((512 / kCols + 1) * kSmem > 228 * 1024, "CTAs an SM");
 };
 
 struct MxArgs {
@@ -89,7 +98,7 @@ struct MxArgs {
     int M, N;                      // rows of X before slicing, output features
     int64_t K, G;                  // columns, 128-column groups
     int MB, KT, CS;                // X tiles, K tiles, CTAs per output tile
-    int lper;                      // log2 of the columns a CTA of a cluster adds up
+    int lper;                      // log2 of the columns a CTA of a cluster adds up, at least 2
     int slices;                    // 1, or kMxSlices columns of D per row of X
     int out;                       // type of Y
 };
@@ -110,40 +119,89 @@ __device__ __forceinline__ __half to<__half>(float v) { return __float2half_rn(v
 template <>
 __device__ __forceinline__ __nv_bfloat16 to<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
+// Four columns m0 .. m0 + 3 (those below M) of feature n to Y.
 template <class T>
-struct alignas(4 * sizeof(T)) Vec4 {
-    T v[4];
-};
+__device__ __forceinline__ void store4(const MxArgs &a, int64_t m0, int64_t n, const float (&y)[4]) {
+    T *dst = static_cast<T *>(a.Y) + m0 * a.ldy + n;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        if (m0 + e < a.M) *dst = to<T>(y[e]);
+        dst += a.ldy;
+    }
+}
 
-// Y's columns first .. first + count of this tile: the CS parts (in CTA order)
-// of [column][128 features], four features a thread, to Y.
-template <class T>
-__device__ __forceinline__ void sum_parts(const MxArgs &a, const float *part, int tid, int count, int64_t m0,
-                                          int64_t n0) {
-    const size_t stride = (size_t)kTileN << a.lper;            // floats of a part
-    const bool vec = a.ldy % 4 == 0;
-    T *const Y = static_cast<T *>(a.Y) + m0 * a.ldy + n0;
-#pragma unroll 4
-    for (int i = tid; i < count * 32; i += 128) {
-        const int col = i >> 5, r = (i & 31) * 4;
-        const float *p = part + (size_t)col * kTileN + r;
-        float4 y = *reinterpret_cast<const float4 *>(p);
-        for (int c = 1; c < a.CS; ++c) {
-            const float4 z = *reinterpret_cast<const float4 *>(p + c * stride);
-            y.x += z.x;
-            y.y += z.y;
-            y.z += z.z;
-            y.w += z.w;
-        }
-        T *const dst = Y + col * a.ldy + r;
-        const Vec4<T> v = {{to<T>(y.x), to<T>(y.y), to<T>(y.z), to<T>(y.w)}};
-        if (vec && n0 + r + 3 < a.N) {
-            *reinterpret_cast<Vec4<T> *>(dst) = v;
+// The accumulator's `live` columns (for SLICES eight of them add to one) of this
+// thread's row, four at a time, to put(column, values).
+template <int BN, class Put>
+__device__ __forceinline__ void read_columns(uint32_t base, int slices, int live, Put put) {
+    constexpr int kStep = BN < 32 ? BN : 32;
+#pragma unroll 1
+    for (int c = 0; c < BN; c += kStep) {
+        if (c / slices >= live) break;
+        uint32_t v[kStep];
+        if constexpr (kStep == 8) tmem_ld8(base + c, v);
+        else if constexpr (kStep == 16) tmem_ld16(base + c, v);
+        else tmem_ld32(base + c, v);
+        tmem_ld_wait();
+        if (slices == kMxSlices) {
+            float y[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int e = 0; e < kStep / kMxSlices; ++e) {             // small slices first
+                y[e] = __uint_as_float(v[kMxSlices * e + kMxSlices - 1]);
+#pragma unroll
+                for (int j = kMxSlices - 2; j >= 0; --j) y[e] += __uint_as_float(v[kMxSlices * e + j]);
+            }
+            put(c / kMxSlices, y);
         } else {
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (n0 + r + e < a.N) dst[e] = v.v[e];
+            for (int g = 0; g < kStep / 4; ++g) {
+                const float y[4] = {__uint_as_float(v[4 * g]), __uint_as_float(v[4 * g + 1]),
+                                    __uint_as_float(v[4 * g + 2]), __uint_as_float(v[4 * g + 3])};
+                if (c + 4 * g < live) put(c + 4 * g, y);
+            }
         }
+    }
+}
+
+// Epilogue of one thread: its row of the tile, straight to Y or in parts to the
+// CTAs that own the columns, which then add what they were sent.
+template <int BN, class T>
+__device__ __forceinline__ void epilogue(const MxArgs &a, uint32_t base, float *parts, uint64_t *sent, int rank,
+                                         int live, int64_t m0, int64_t n, int row, bool ok, volatile int *flags) {
+    if (a.CS == 1) {
+        if (ok)
+            read_columns<BN>(base, a.slices, live, [&](int col, const float (&y)[4]) {
+                if (n < a.N) store4<T>(a, m0 + col, n, y);
+            });
+        return;
+    }
+    const int lper = a.lper, first = rank << lper, left = live - first, per = 1 << lper;
+    const int groups = ((left < per ? left : per) + 3) / 4;   // of four columns owned; <= 0: none
+    float4 *const p4 = reinterpret_cast<float4 *>(parts);     // [CTA][group][row]
+    if (ok) {
+        const uint32_t to0 = smem_u32(p4 + ((size_t)rank << (lper - 2)) * kTileN + row), bar0 = smem_u32(sent);
+        read_columns<BN>(base, a.slices, live, [&](int col, const float (&y)[4]) {
+            const uint32_t owner = (uint32_t)(col >> lper), at = to0 + (uint32_t)((col & (per - 1)) >> 2) * (kTileN * 16);
+            st_async_v4(cluster_map(at, owner), y[0], y[1], y[2], y[3], cluster_map(bar0, owner));
+        });
+    }
+    if (groups <= 0) return;
+    // never cut short, also when this CTA gave up: until then stores to this
+    // CTA's memory may be on their way
+    const bool got = mbar_wait_bounded(sent, 0);
+    if (!got) flags[0] = 1;
+    if (!got || !ok) return;
+#pragma unroll 2
+    for (int g = 0; g < groups; ++g) {
+        float y[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int c = 0; c < a.CS; ++c) {                      // in CTA order
+            const float4 z = p4[(((size_t)c << (lper - 2)) + g) * kTileN + row];
+            y[0] += z.x;
+            y[1] += z.y;
+            y[2] += z.z;
+            y[3] += z.w;
+        }
+        if (n < a.N) store4<T>(a, m0 + first + 4 * g, n, y);
     }
 }
 
@@ -155,9 +213,10 @@ mx4_gemm_kernel(const __grid_constant__ MxArgs a) {
     constexpr int kPrefetch = 16;                // stages brought into L2 ahead
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    uint64_t *full = reinterpret_cast<uint64_t *>(smem + kS * C::kStage), *empty = full + kS, *done = empty + kS;
-    volatile int *flags = reinterpret_cast<volatile int *>(done + 1);   // [0] abort [1] loads [2] MMA stages
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(done + 1) + 4;
+    float *parts = reinterpret_cast<float *>(smem + kS * C::kStage);
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + kS * C::kStage + C::kParts), *empty = full + kS, *done = empty + kS, *sent = done + 1;
+    volatile int *flags = reinterpret_cast<volatile int *>(sent + 1);   // [0] abort [1] loads [2] MMA stages
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sent + 1) + 4;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = a.CS > 1 ? (int)(blockIdx.x % a.CS) : 0;
@@ -165,16 +224,19 @@ mx4_gemm_kernel(const __grid_constant__ MxArgs a) {
     const int k0 = (int)((int64_t)rank * a.KT / a.CS), k1 = (int)((int64_t)(rank + 1) * a.KT / a.CS);
 
     if (threadIdx.x == 0) {
+        if (!FUSED) prefetch_tensormap(&a.xmap);
         for (int i = 0; i < kPrefetch && i < k1 - k0; ++i) tma_prefetch_2d(&a.wmap, (k0 + i) * 128, t * kTileN);
         for (int i = 0; i < kS; ++i) {
             mbar_init(full + i, FUSED ? 1 + a.M : 1);   // the loads and the slicing warps
             mbar_init(empty + i, 1);
         }
         mbar_init(done, 1);
+        mbar_init(sent, 1);
         flags[0] = flags[1] = flags[2] = 0;
         fence_mbar_init();
     }
     __syncthreads();
+    if (a.CS > 1) cluster_arrive();              // this CTA's barriers are ready (waited for before the parts)
     // the operands may come from the previous kernel; tensor memory is taken
     // after it too, so that it never waits for columns held here
     pdl_wait();
@@ -312,70 +374,22 @@ mx4_gemm_kernel(const __grid_constant__ MxArgs a) {
     const int cols = BN / a.slices;                           // rows of X of this tile
     const int64_t m0 = (int64_t)mb * cols;
     const int live = a.M - m0 < cols ? (int)(a.M - m0) : cols;
-    const int lper = a.lper, per = 1 << lper;                 // columns a CTA owns
-    float *part = reinterpret_cast<float *>(smem);            // [CTA][owned column][128], once the rings are idle
-    bool ok = true;
+    if (a.CS > 1) cluster_wait();
     if (warp >= kEpiW0) {
-        ok = mbar_wait_backoff(done, 0, flags);
+        if (a.CS > 1 && threadIdx.x == 32 * kEpiW0) {
+            const int left = live - (rank << a.lper), own = left < (1 << a.lper) ? left : 1 << a.lper;
+            if (own > 0) mbar_expect_tx(sent, (uint32_t)a.CS * (uint32_t)((own + 3) / 4) * (kTileN * 16));
+        }
+        bool ok = mbar_wait_backoff(done, 0, flags);
         ok = __all_sync(0xFFFFFFFFu, ok);
-    }
-    if (a.CS > 1) {
-        __syncwarp();
-        cluster_arrive();                                     // every CTA's ring is idle
-        cluster_wait();
-    }
-    if (warp >= kEpiW0) {
         named_sync(1, 160);
         tc_fence_after();
-        if (ok) {
-            const uint32_t base = *reinterpret_cast<volatile uint32_t *>(tmem_slot) + C::kD + ((uint32_t)(32 * q) << 16);
-            const uint32_t mine = smem_u32(part + ((size_t)rank << lper) * kTileN + row);
-            constexpr int kStep = BN < 32 ? BN : 32;
-#pragma unroll 1
-            for (int c = 0; c < BN; c += kStep) {
-                if (c / a.slices >= live) break;
-                uint32_t v[kStep];
-                if constexpr (kStep == 8) tmem_ld8(base + c, v);
-                else if constexpr (kStep == 16) tmem_ld16(base + c, v);
-                else tmem_ld32(base + c, v);
-                tmem_ld_wait();
-                auto put = [&](int col, float y) {            // columns beyond live stay inside the parts
-                    if (a.CS > 1)
-                        st_cluster_f32(cluster_map(mine + (uint32_t)((col & (per - 1)) * kTileN * 4), (uint32_t)(col >> lper)), y);
-                    else
-                        part[col * kTileN + row] = y;
-                };
-                if (a.slices == kMxSlices) {                  // small slices first
-#pragma unroll
-                    for (int e = 0; e < kStep / kMxSlices; ++e) {
-                        float s = __uint_as_float(v[kMxSlices * e + kMxSlices - 1]);
-#pragma unroll
-                        for (int j = kMxSlices - 2; j >= 0; --j) s += __uint_as_float(v[kMxSlices * e + j]);
-                        put(c / kMxSlices + e, s);
-                    }
-                } else {
-#pragma unroll
-                    for (int j = 0; j < kStep; ++j) put(c + j, __uint_as_float(v[j]));
-                }
-            }
-        }
+        const uint32_t base = *reinterpret_cast<volatile uint32_t *>(tmem_slot) + C::kD + ((uint32_t)(32 * q) << 16);
+        const int64_t n = (int64_t)t * kTileN + row;
+        if (a.out == MQ_BF16) epilogue<BN, __nv_bfloat16>(a, base, parts, sent, rank, live, m0, n, row, ok, flags);
+        else if (a.out == MQ_F16) epilogue<BN, __half>(a, base, parts, sent, rank, live, m0, n, row, ok, flags);
+        else epilogue<BN, float>(a, base, parts, sent, rank, live, m0, n, row, ok, flags);
         tc_fence_before();
-    }
-    if (a.CS > 1) {
-        __syncwarp();
-        cluster_arrive();
-        cluster_wait();
-    }
-    if (warp >= kEpiW0) {
-        if (a.CS == 1) named_sync(2, 128);
-        const int first = rank << lper, count = live - first < per ? live - first : per;
-        const int tid = threadIdx.x - 32 * kEpiW0;
-        const int64_t n0 = (int64_t)t * kTileN;
-        if (ok && count > 0) {
-            if (a.out == MQ_BF16) sum_parts<__nv_bfloat16>(a, part, tid, count, m0 + first, n0);
-            else if (a.out == MQ_F16) sum_parts<__half>(a, part, tid, count, m0 + first, n0);
-            else sum_parts<float>(a, part, tid, count, m0 + first, n0);
-        }
     }
 
     // ---- end: copies and MMAs in flight land (already so unless a wait gave up)
@@ -445,11 +459,11 @@ mq_status launch(const MxProduct &p, cudaStream_t st) {
     a.slices = p.slices;
     a.out = p.out;
     const int64_t tiles = (w->rows + kTileN - 1) / kTileN * a.MB;
-    // K is split while the CTAs still fit the GPU once (two an SM up to 64
-    // columns) and each keeps two stages of K
+    // K is split while the CTAs still fit the GPU once (kPerSm an SM) and each keeps kMinStages of K (two
+    // stages each: 7.2 us for 16 x 4096 x 4096, four: 5.3, six: 6.4)
     a.CS = 1;
-    while (a.CS < 8 && tiles * a.CS * 2 <= (BN <= 64 ? MX_FILL2 : MX_FILL1) && a.KT >= a.CS * 4) a.CS *= 2;
-    for (a.lper = 0; (a.CS << a.lper) < BN / p.slices;) ++a.lper;
+    while (a.CS < 8 && tiles * a.CS * 2 <= (BN <= 32 ? 296 : 148) && a.KT >= a.CS * 2 * kMinStages) a.CS *= 2;
+    for (a.lper = 2; (a.CS << a.lper) < BN / p.slices;) ++a.lper;
     if (tiles * a.CS > 0x7FFFFFFF) return fail(MQ_ERR_UNSUPPORTED, "mq_mx4_gemm: too many output tiles");
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
