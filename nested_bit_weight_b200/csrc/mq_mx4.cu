@@ -95,13 +95,6 @@ struct Raw8<MQ_F32> {
     }
 };
 
-// The four scale bytes of 128 columns (16 lanes), gathered in each lane.
-__device__ __forceinline__ uint32_t gather_scales(uint32_t E, int lane) {
-    uint32_t w = E << (8 * ((lane >> 2) & 3));
-    w |= __shfl_xor_sync(0xFFFFFFFFu, w, 4);
-    return w | __shfl_xor_sync(0xFFFFFFFFu, w, 8);
-}
-
 // Rows per warp and step: so many 16-byte loads of a thread are in flight.
 __host__ __device__ constexpr int quant_rows(int dtype) { return dtype == MQ_F32 ? 4 : 8; }
 constexpr int kDeqRows = 8;
@@ -114,6 +107,8 @@ __global__ void __launch_bounds__(256)
 mx_quantize_kernel(const uint8_t *__restrict__ X, int64_t rows, int64_t K, int64_t ld_bytes,
                    uint8_t *__restrict__ codes, uint8_t *__restrict__ scales) {
     constexpr int kRows = quant_rows(DT);
+    sm100::pdl_wait();
+    sm100::pdl_launch_dependents();
     const int lane = threadIdx.x & 31;
     const int64_t G = mx_groups(K), C = (K + 255) / 256, steps = (rows + 127) / 128 * (128 / kRows);
     const int64_t total = steps * C, nwarps = ((int64_t)gridDim.x * blockDim.x) >> 5;
@@ -143,19 +138,25 @@ mx_quantize_kernel(const uint8_t *__restrict__ X, int64_t rows, int64_t K, int64
     }
 }
 
-// Row m of bf16 X to the rows 8 m .. 8 m + 7 of an MXFP4 matrix whose sum it
-// is (mq_mx4.cuh).  One warp: 256 columns of one row.
+// Row m of bf16 X to S rows of an MXFP4 matrix whose sum it is (mq_mx4.cuh), in
+// tiles of `tpt` rows of X: codes in row tile * bn + (m % tpt) * S + j, scales in
+// row band_rows * tile + (m % tpt) * S + j.  Rows and columns between are not
+// written: their products fall into columns that nothing reads.  One warp: 256
+// columns of one row.
+template <int S>
 __global__ void __launch_bounds__(256)
-mx_slices_kernel(const uint8_t *__restrict__ X, int64_t M, int64_t K, int64_t ld_bytes,
-                 uint8_t *__restrict__ codes, uint8_t *__restrict__ scales) {
+mx_slices_kernel(const uint8_t *__restrict__ X, int64_t M, int64_t K, int64_t ld_bytes, int tpt, int bn,
+                 int band_rows, uint8_t *__restrict__ codes, uint8_t *__restrict__ scales) {
     sm100::pdl_wait();                        // X may come from the previous kernel
+    sm100::pdl_launch_dependents();
     const int lane = threadIdx.x & 31;
-    const int64_t G = mx_groups(K), C = (K + 255) / 256, Mp = (M + 15) / 16 * 16;
-    const int64_t total = Mp * C, nwarps = ((int64_t)gridDim.x * blockDim.x) >> 5;
+    const int64_t G = mx_groups(K), C = (K + 255) / 256;
+    const int64_t total = M * C, nwarps = ((int64_t)gridDim.x * blockDim.x) >> 5;
     for (int64_t i = (blockIdx.x * (int64_t)blockDim.x + threadIdx.x) >> 5; i < total; i += nwarps) {
-        const int64_t m = i / C, c = (i % C) * 256 + lane * 8;
+        const int64_t m = i / C, c = (i % C) * 256 + lane * 8, tile = m / tpt;
+        const int local = (int)(m - tile * tpt) * S;
         Raw8<MQ_BF16> raw;
-        if (m < M && c < K) raw.load(X + m * ld_bytes + c * 2);
+        if (c < K) raw.load(X + m * ld_bytes + c * 2);
         else raw.zero();
         float u[8];
         raw.get(u);
@@ -164,15 +165,14 @@ mx_slices_kernel(const uint8_t *__restrict__ X, int64_t M, int64_t K, int64_t ld
         const float inv = bad ? 0.f : mx_inverse(E);
 #pragma unroll
         for (int e = 0; e < 8; ++e) u[e] = bad ? 0.f : u[e] * inv;
+        uint8_t *dst = codes + (tile * bn + local) * (K / 2) + c / 2;
 #pragma unroll
-        for (int j = 0; j < kMxSlices; ++j) {
-            const int64_t row = m * kMxSlices + j;
-            const uint32_t sw = gather_scales(E, lane);
-            if ((lane & 15) == 0 && c < G * 128)
-                *reinterpret_cast<uint32_t *>(scales + mx_scale_at(row, c >> 7, G)) = sw;
+        for (int j = 0; j < S; ++j) {
+            if ((lane & 3) == 0 && c < G * 128)
+                scales[mx_scale_at(tile * band_rows + local + j, c >> 7, G) + ((lane >> 2) & 3)] = (uint8_t)E;
             const uint32_t En = mx_next_slice(E, j);
             const uint32_t code = mx_slice_codes(u, E - En);
-            if (m < M && c < K) *reinterpret_cast<uint32_t *>(codes + row * (K / 2) + c / 2) = code;
+            if (c < K) *reinterpret_cast<uint32_t *>(dst + j * (K / 2)) = code;
             E = En;
         }
     }
@@ -183,6 +183,8 @@ template <bool F32>
 __global__ void __launch_bounds__(256)
 mx_dequantize_kernel(const uint8_t *__restrict__ codes, const uint8_t *__restrict__ scales, int64_t rows,
                      int64_t K, uint8_t *__restrict__ out, int64_t ld_bytes) {
+    sm100::pdl_wait();
+    sm100::pdl_launch_dependents();
     const int lane = threadIdx.x & 31;
     const int64_t G = mx_groups(K), C = (K + 255) / 256, steps = (rows + kDeqRows - 1) / kDeqRows;
     const int64_t total = steps * C, nwarps = ((int64_t)gridDim.x * blockDim.x) >> 5;
@@ -295,6 +297,8 @@ __global__ void __launch_bounds__(256)
 mx_from_nested_kernel(const uint32_t *__restrict__ planes, const uint16_t *__restrict__ s16,
                       const uint16_t *__restrict__ z16, int64_t N, int64_t K,
                       uint8_t *__restrict__ codes, uint8_t *__restrict__ scales) {
+    sm100::pdl_wait();
+    sm100::pdl_launch_dependents();
     const int64_t G = K / kGroup, blocks = (N + 127) / 128 * G, plane_words = blocks * 512;
     const int w = threadIdx.x & 3, n0 = (int)(threadIdx.x >> 2);     // word and first row of this thread
     for (int64_t block = blockIdx.x; block < blocks; block += gridDim.x) {
@@ -327,6 +331,22 @@ int grid_for(int64_t work, int per_block) {
     return (int)(g < 1 ? 1 : g);
 }
 
+// 256 threads a block, allowed to start before the previous kernel has ended
+// (every kernel here waits for it before it reads or writes anything).
+template <class... P, class... A>
+cudaError_t launch_pdl(void (*fn)(P...), int grid, cudaStream_t st, A... args) {
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(256);
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, fn, static_cast<P>(args)...);
+}
+
 bool mx_sizes(int64_t rows, int64_t K) {
     return rows >= 0 && rows <= kMxMaxDim && K >= kMxBlock && K % kMxBlock == 0 && K <= kMxMaxDim;
 }
@@ -344,19 +364,11 @@ mq_status check_mx4(const mq_mx4 *m, const char *what) {
     return MQ_OK;
 }
 
-mq_status launch_mx_slices(const uint16_t *X, int64_t M, int64_t K, int64_t ldx, uint8_t *codes,
-                           uint8_t *scales, cudaStream_t st) {
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)grid_for((M + 15) / 16 * 16 * ((K + 255) / 256) * 32, 256));
-    cfg.blockDim = dim3(256);
-    cfg.stream = st;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, mx_slices_kernel, reinterpret_cast<const uint8_t *>(X), M, K,
-                                             ldx * 2, codes, scales);
+mq_status launch_mx_slices(const uint16_t *X, int64_t M, int64_t K, int64_t ldx, const MxSlicing &sl,
+                           uint8_t *codes, uint8_t *scales, cudaStream_t st) {
+    const cudaError_t e =
+        launch_pdl(sl.S == 6 ? mx_slices_kernel<6> : mx_slices_kernel<8>, grid_for(M * ((K + 255) / 256) * 32, 256), st,
+                   reinterpret_cast<const uint8_t *>(X), M, K, ldx * 2, sl.tpt, sl.bn, sl.Tb ? 256 : 128, codes, scales);
     return e == cudaSuccess ? MQ_OK : cuda_fail(e, "mx_slices_kernel");
 }
 
@@ -390,13 +402,10 @@ extern "C" mq_status mq_mx4_quantize(const void *X, int dtype, int64_t rows, int
     if (bs != MQ_OK) return bs;
     const int grid = grid_for((rows + 127) / 128 * (128 / quant_rows(dtype)) * ((K + 255) / 256) * 32, 256);
     const uint8_t *x = static_cast<const uint8_t *>(X);
-    if (dtype == MQ_BF16)
-        mx_quantize_kernel<MQ_BF16><<<grid, 256, 0, st>>>(x, rows, K, ld * size, codes_out, scales_out);
-    else if (dtype == MQ_F16)
-        mx_quantize_kernel<MQ_F16><<<grid, 256, 0, st>>>(x, rows, K, ld * size, codes_out, scales_out);
-    else
-        mx_quantize_kernel<MQ_F32><<<grid, 256, 0, st>>>(x, rows, K, ld * size, codes_out, scales_out);
-    const cudaError_t e = cudaGetLastError();
+    const auto fn = dtype == MQ_BF16  ? mx_quantize_kernel<MQ_BF16>
+                    : dtype == MQ_F16 ? mx_quantize_kernel<MQ_F16>
+                                      : mx_quantize_kernel<MQ_F32>;
+    const cudaError_t e = launch_pdl(fn, grid, st, x, rows, K, ld * size, codes_out, scales_out);
     return e == cudaSuccess ? MQ_OK : cuda_fail(e, "mx_quantize_kernel");
 }
 
@@ -416,8 +425,7 @@ extern "C" mq_status mq_mx4_from_nested(const mq_weights *w, uint8_t *codes_out,
                               mx_from_nested_kernel<4>, mx_from_nested_kernel<5>, mx_from_nested_kernel<6>,
                               mx_from_nested_kernel<7>, mx_from_nested_kernel<8>};
     const int grid = grid_for((w->N + 127) / 128 * (w->K / kGroup), 1);
-    fns[w->r - 1]<<<grid, 256, 0, st>>>(w->planes, w->scales, w->zeros, w->N, w->K, codes_out, scales_out);
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e = launch_pdl(fns[w->r - 1], grid, st, w->planes, w->scales, w->zeros, w->N, w->K, codes_out, scales_out);
     return e == cudaSuccess ? MQ_OK : cuda_fail(e, "mx_from_nested_kernel");
 }
 
@@ -436,10 +444,7 @@ extern "C" mq_status mq_mx4_dequantize(const mq_mx4 *m, void *out, int dtype, in
     if ((s = bind_device(st)) != MQ_OK) return s;
     const int grid = grid_for((m->rows + kDeqRows - 1) / kDeqRows * ((m->K + 255) / 256) * 32, 256);
     uint8_t *o = static_cast<uint8_t *>(out);
-    if (dtype == MQ_F32)
-        mx_dequantize_kernel<true><<<grid, 256, 0, st>>>(m->codes, m->scales, m->rows, m->K, o, ld * size);
-    else
-        mx_dequantize_kernel<false><<<grid, 256, 0, st>>>(m->codes, m->scales, m->rows, m->K, o, ld * size);
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e = launch_pdl(dtype == MQ_F32 ? mx_dequantize_kernel<true> : mx_dequantize_kernel<false>, grid, st,
+                                     m->codes, m->scales, m->rows, m->K, o, ld * size);
     return e == cudaSuccess ? MQ_OK : cuda_fail(e, "mx_dequantize_kernel");
 }

@@ -25,8 +25,16 @@ bool mx_encode_scales(CUtensorMap *map, const uint8_t *scales, int64_t rows, int
 // rows, 128-byte swizzle; the row stride must be a multiple of 16 bytes.
 bool mx_encode_y(CUtensorMap *map, void *Y, int64_t M, int64_t N, int64_t ldy, int out);
 
-// One product: X of M * slices MXFP4 rows (slices > 1: sums of that many
-// consecutive rows, mq_mx4_gemm_bf16), w of N rows.
+// How M bf16 rows lie as MXFP4 rows (a workspace of the product): S slices a row,
+// `tpt` rows of X a tile of `bn` MXFP4 rows; a tile's scales start a row band of
+// their own.  Tb = 0: one tile, of the kernel for few rows.
+struct MxSlicing {
+    int S, Tb, tpt, bn;
+    int64_t rows, bands;           // MXFP4 rows, row bands of scales
+};
+MxSlicing mx_slicing(int64_t M, int out);
+
+// One product: X of M MXFP4 rows (slices = 1) or as laid out by `slice`, w of N rows.
 struct MxProduct {
     const uint8_t *xcodes, *xscales;
     int64_t M;
@@ -37,6 +45,7 @@ struct MxProduct {
     int64_t ldy;
     const uint16_t *X;             // bf16 rows cut within the product (few rows), or NULL
     int64_t ldx;
+    MxSlicing slice;
 };
 bool mx_pair_takes(const MxProduct &p);
 mq_status launch_mx_pair(const MxProduct &p, cudaStream_t st);
@@ -100,13 +109,14 @@ __device__ __forceinline__ void mx_units8(uint32_t codes, float (&u)[8]) {
     }
 }
 
-// ---- bf16 rows as sums of kMxSlices MXFP4 rows.  With a = max |x| of a
+// ---- bf16 rows as sums of MXFP4 rows.  With a = max |x| of a
 // block, slice 0 has the least unit 2^e0 with a <= 7 * 2^e0: rounding to the
 // grid leaves at most 1 unit (up to 5 by half a step, above 5 to 6).  In units
 // a quarter as large that rest is at most 4, where the grid's half step is
-// 1/2; in units an eighth as large again at most 4, and so on.  After eight
-// slices the rest is at most 2^(e0 - 21), below 2^-22 a (a > 3.5 * 2^e0).
-constexpr int kMxSlices = 8;
+// 1/2; in units an eighth as large again at most 4, and so on.  After S slices
+// the rest is at most 2^(e0 - 3 (S - 1)): below 2^-22 a with eight, 2^-16 a with
+// six (a > 3.5 * 2^e0).
+constexpr int kMxSlices = 8;                 // slices unless mx_slicing takes fewer
 
 __device__ __forceinline__ uint32_t mx_slice0_byte(uint32_t amax) {
     const uint32_t f = (amax >> 23) + ((amax & 0x7FFFFFu) > 0x600000u ? 1u : 0u);   // a > 1.75 * 2^k

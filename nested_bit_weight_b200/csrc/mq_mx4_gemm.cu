@@ -41,8 +41,8 @@
 #include "mq_sm100.cuh"
 
 namespace mq {
-mq_status launch_mx_slices(const uint16_t *X, int64_t M, int64_t K, int64_t ldx, uint8_t *codes,
-                           uint8_t *scales, cudaStream_t st);
+mq_status launch_mx_slices(const uint16_t *X, int64_t M, int64_t K, int64_t ldx, const MxSlicing &sl,
+                           uint8_t *codes, uint8_t *scales, cudaStream_t st);
 namespace {
 
 using namespace sm100;
@@ -491,10 +491,12 @@ mq_status check_y(const char *what, int64_t N, const void *Y, int dtype, int64_t
     return MQ_OK;
 }
 
+// Rows of bf16 X at most: their slices, with the rows that fill up tiles, are
+// numbered in 32 bits.
+constexpr int64_t kMaxRows = (int64_t)1 << 27;
+
 // Workspace of mq_mx4_gemm_bf16: the slices' codes, then their scales.
-size_t slice_code_bytes(int64_t M, int64_t K) {
-    return ((size_t)M * kMxSlices * (size_t)(K / 2) + 15) / 16 * 16;
-}
+size_t slice_code_bytes(const MxSlicing &sl, int64_t K) { return ((size_t)sl.rows * (size_t)(K / 2) + 15) / 16 * 16; }
 
 }  // namespace
 
@@ -573,14 +575,16 @@ extern "C" mq_status mq_mx4_gemm(const mq_mx4 *X, const mq_mx4 *w, void *Y, int 
     if ((s = check_y("mq_mx4_gemm", w->rows, Y, y_dtype, ldy)) != MQ_OK) return s;
     cudaStream_t st = (cudaStream_t)stream;
     if ((s = bind_device(st)) != MQ_OK) return s;
-    return launch(MxProduct{X->codes, X->scales, X->rows, 1, w, Y, y_dtype, ldy, nullptr, 0}, st);
+    return launch(MxProduct{X->codes, X->scales, X->rows, 1, w, Y, y_dtype, ldy, nullptr, 0, {}}, st);
 }
 
 extern "C" size_t mq_mx4_gemm_bf16_workspace_bytes(int64_t M, int64_t N, int64_t K) {
-    if (M < 1 || M > kMxMaxDim / kMxSlices || N < 1 || N > kMxMaxDim || K < kMxBlock || K % kMxBlock || K > kMxMaxDim)
+    if (M < 1 || M > kMaxRows || N < 1 || N > kMxMaxDim || K < kMxBlock || K % kMxBlock || K > kMxMaxDim)
         return 0;
     if (M <= kFusedRows) return 0;
-    return slice_code_bytes(M, K) + mq_mx4_scale_bytes(M * kMxSlices, K);
+    // the larger of the layouts (MQ_F32 takes more slices)
+    const MxSlicing sl = mx_slicing(M, MQ_F32);
+    return slice_code_bytes(sl, K) + (size_t)sl.bands * (size_t)mx_groups(K) * 512;
 }
 
 extern "C" mq_status mq_mx4_gemm_bf16(const uint16_t *X, int64_t M, int64_t ldx, const mq_mx4 *w, void *Y,
@@ -589,7 +593,7 @@ extern "C" mq_status mq_mx4_gemm_bf16(const uint16_t *X, int64_t M, int64_t ldx,
     mq_status s = check_mx4(w, "mq_mx4_gemm_bf16 (w)");
     if (s != MQ_OK) return s;
     if (w->rows < 1) return fail(MQ_ERR_INVALID_ARG, "mq_mx4_gemm_bf16: w has no rows");
-    if (M < 0 || M > kMxMaxDim / kMxSlices) return fail(MQ_ERR_INVALID_ARG, "mq_mx4_gemm_bf16: M out of range");
+    if (M < 0 || M > kMaxRows) return fail(MQ_ERR_INVALID_ARG, "mq_mx4_gemm_bf16: M out of range");
     if (M == 0) return MQ_OK;
     if (!X) return fail(MQ_ERR_INVALID_ARG, "mq_mx4_gemm_bf16: X is NULL");
     if (ldx < w->K || ldx > INT64_MAX / 8) return fail(MQ_ERR_INVALID_ARG, "mq_mx4_gemm_bf16: need ldx >= K");
@@ -601,11 +605,18 @@ extern "C" mq_status mq_mx4_gemm_bf16(const uint16_t *X, int64_t M, int64_t ldx,
         return fail(MQ_ERR_WORKSPACE, "workspace smaller than mq_mx4_gemm_bf16_workspace_bytes");
     cudaStream_t st = (cudaStream_t)stream;
     if ((s = bind_device(st)) != MQ_OK) return s;
-    if (M <= kFusedRows)
-        return launch(MxProduct{nullptr, nullptr, M, kMxSlices, w, Y, y_dtype, ldy, X, ldx}, st);
-    uint8_t *codes = static_cast<uint8_t *>(workspace), *scales = codes + slice_code_bytes(M, w->K);
-    if ((s = launch_mx_slices(X, M, w->K, ldx, codes, scales, st)) != MQ_OK) return s;
-    return launch(MxProduct{codes, scales, M, kMxSlices, w, Y, y_dtype, ldy, nullptr, 0}, st);
+    MxProduct p{nullptr, nullptr, M, kMxSlices, w, Y, y_dtype, ldy, nullptr, 0, {}};
+    if (M <= kFusedRows) {
+        p.X = X;
+        p.ldx = ldx;
+        return launch(p, st);
+    }
+    p.slice = mx_slicing(M, y_dtype);
+    uint8_t *codes = static_cast<uint8_t *>(workspace), *scales = codes + slice_code_bytes(p.slice, w->K);
+    if ((s = launch_mx_slices(X, M, w->K, ldx, p.slice, codes, scales, st)) != MQ_OK) return s;
+    p.xcodes = codes;
+    p.xscales = scales;
+    return launch(p, st);
 }
 
 #ifdef MQ_TEST_HOOKS

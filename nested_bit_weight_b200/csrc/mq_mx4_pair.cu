@@ -5,17 +5,20 @@
 // of B as well: the bytes that feed one MMA halve against single CTAs, and the
 // 4-bit rate is so high (16384 products a clock and SM) that those bytes, from
 // L2 through shared memory, are what bounds a large product.
-//   rows form     A = X, B = w: a lane holds a row of Y, BN consecutive features;
-//                 32 x 64 pieces go through shared memory to TMA stores.
-//   slices form   A = w, B = X (bf16 activations as sums of eight MXFP4 rows): a
-//                 lane holds a feature; eight columns of D add to one output.
+//   rows form     (S = 0) A = X, B = w: a lane holds a row of Y, BN consecutive
+//                 features; 32-row pieces go through shared memory to TMA stores.
+//   columns form  (S >= 1) A = w, B = X: a lane holds a feature, so that a warp
+//                 stores 32 neighbours of a row of Y whatever Y's alignment.  S = 1
+//                 where Y does not allow TMA stores, S = 6 or 8 for bf16
+//                 activations: S columns of D add to one output.
 //
 // Persistent clusters, tiles dealt in turn (rows of A fastest, so that the
 // clusters at work share B tiles in L2).  Tensor memory: two accumulators and
 // the scales of every stage of the shared-memory ring (a stage's scales are
-// overwritten only once its MMAs are done, with no wait of their own).  That is
-// more than 512 columns, so the accumulators overlap by half (0..255, 128..383);
-// the epilogue reads the shared half first and lets the next tile's MMAs start.
+// overwritten only once its MMAs are done, with no wait of their own).  With 256
+// columns that is more than 512, so the accumulators overlap by half (0..255,
+// 128..383); the epilogue reads the shared half first and lets the next tile's
+// MMAs start.
 //
 // Roles: a loading warp (both CTAs' loads complete on the even CTA's barrier), a
 // warp of the even CTA that issues the MMAs, four epilogue warps.  Waits are
@@ -24,6 +27,7 @@
 #include <cuda.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "mq_mx4.cuh"
 #include "mq_sm100.cuh"
@@ -45,30 +49,31 @@ __device__ int g_test_drop_pair;             // as in the single-CTA kernel
 
 template <int BN>
 struct PairCfg {
-    static constexpr int kBands = BN / 128;
+    static constexpr int kBands = BN > 128 ? 2 : 1;                  // scale bands loaded for B
     static constexpr uint32_t kA = 128 * 128, kB = BN / 2 * 128;     // codes of a stage and CTA
     static constexpr uint32_t kSfA = 1024, kSfB = 1024 * kBands;
     static constexpr uint32_t kStage = kA + kB + kSfA + kSfB;
-    static constexpr int kStages = BN == 256 ? 5 : 7;
+    static constexpr int kStages = BN > 128 ? 5 : 7;
     static constexpr uint32_t kStg = 4096;                           // one 32-row piece of Y
     static constexpr int kLag = BN == 256 ? 1 : 2;                   // tiles until the accumulator is needed again
-    static constexpr uint32_t kD1 = 128;                             // second accumulator
-    static constexpr uint32_t kSf = kD1 + BN, kSfCols = 8 + 8 * kBands;
-    static_assert(kSf + kStages * kSfCols <= 512, "TMEM columns");
+    static constexpr uint32_t kD1 = BN == 256 ? 128 : 192;           // second accumulator
+    static constexpr uint32_t kSf = 384, kSfCols = 8 + 8 * kBands;   // scales of the stages
+    static_assert(kD1 + BN <= kSf && kSf + kStages * kSfCols <= 512, "TMEM columns");
     static constexpr size_t kSmem = 1024 + (size_t)kStages * kStage + 8 * kStg + 512;
     static_assert(kSmem <= 227 * 1024 && kStage % 1024 == 0, "shared memory");
 };
 
 struct PairArgs {
-    CUtensorMap amap, bmap, ymap;  // codes in boxes of 128 and BN / 2 rows; Y
-    CUtensorMap asmap, bsmap;      // scales in boxes of 1 and BN / 128 row bands
+    CUtensorMap amap, bmap, ymap;  // codes in boxes of 128 and bn / 2 rows; Y
+    CUtensorMap asmap, bsmap;      // scales in boxes of 1 and kBands row bands
     void *Y;
     int64_t ldy;
     int M, N;                      // rows of Y, columns of Y
     int64_t K;
     int Ta, Tb, KT;                // tiles along A and B, K tiles
+    int bn;                        // rows of B a tile, a multiple of 16, at most BN
+    int tpt;                       // S > 1: rows of X a tile
     int out;
-    int tma_y;                     // Y's rows allow TMA stores
 };
 
 template <class T>
@@ -93,40 +98,33 @@ __device__ __forceinline__ void stage_row(uint8_t *stg, int lane, const uint32_t
             make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
 }
 
-// The staged piece (rows m0.., 128 bytes from byte x0 of a row) to Y.
-template <int SIZE>
+// The staged piece (32 rows from m0, 128 bytes of columns from n0) to Y.
 __device__ __forceinline__ void store_piece(const PairArgs &a, const uint8_t *stg, int lane, int m0, int n0) {
-    constexpr int kCols = 128 / SIZE;
-    if (m0 >= a.M || n0 >= a.N) {                                    // uniform over the warp
-        if (lane == 0) bulk_commit();                                // an empty group: bulk_wait_read counts pieces
-        return;
-    }
-    if (a.tma_y) {
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-            tma_store_2d(&a.ymap, n0, m0, stg);
-            bulk_commit();
-        }
-    } else {
-        __syncwarp();
-        const int rows = a.M - m0 < 32 ? a.M - m0 : 32;
-        for (int r = 0; r < rows; ++r)
-#pragma unroll
-            for (int h = 0; h < kCols / 32; ++h) {
-                const int col = 32 * h + lane, byte = col * SIZE;
-                const uint8_t *p = stg + r * 128 + (((byte >> 4) ^ (r & 7)) << 4) + (byte & 15);
-                if (n0 + col < a.N) {
-                    const int64_t at = (int64_t)(m0 + r) * a.ldy + n0 + col;
-                    if constexpr (SIZE == 2) static_cast<uint16_t *>(a.Y)[at] = *reinterpret_cast<const uint16_t *>(p);
-                    else static_cast<uint32_t *>(a.Y)[at] = *reinterpret_cast<const uint32_t *>(p);
-                }
-            }
-        __syncwarp();
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+        if (m0 < a.M && n0 < a.N) tma_store_2d(&a.ymap, n0, m0, stg);
+        bulk_commit();                                               // empty or not: bulk_wait_read counts pieces
     }
 }
 
-template <int BN, bool SLICES>
+// `count` values of feature n, rows m0.. of Y.
+template <class T, int COUNT>
+__device__ __forceinline__ void store_column(const PairArgs &a, int m0, int mend, int64_t n, const float (&y)[COUNT]) {
+    if (n >= a.N) return;
+    T *dst = static_cast<T *>(a.Y) + (int64_t)m0 * a.ldy + n;
+#pragma unroll
+    for (int e = 0; e < COUNT; ++e) {
+        if (m0 + e < mend) {
+            if constexpr (sizeof(T) == 4) *dst = y[e];
+            else if constexpr (std::is_same<T, __half>::value) *dst = __float2half_rn(y[e]);
+            else *dst = __float2bfloat16_rn(y[e]);
+        }
+        dst += a.ldy;
+    }
+}
+
+template <int BN, int S>
 __global__ void __launch_bounds__(kThreads, 1)
 mx4_pair_kernel(const __grid_constant__ PairArgs a) {
     using C = PairCfg<BN>;
@@ -155,6 +153,15 @@ mx4_pair_kernel(const __grid_constant__ PairArgs a) {
         flags[0] = flags[2] = 0;
         fence_mbar_init();
     }
+    if (threadIdx.x == 0) {
+        // nothing is read before the wait; the weights only come into L2
+        const CUtensorMap *wmap = S ? &a.amap : &a.bmap;
+        const int y = S ? (cluster % a.Ta) * 256 + rank * 128 : (cluster / a.Ta) * a.bn + rank * (a.bn / 2);
+        for (int kt = 0; kt < kS && kt < a.KT; ++kt) tma_prefetch_2d(wmap, kt * 128, y);
+        prefetch_tensormap(S ? &a.bmap : &a.amap);
+        prefetch_tensormap(&a.asmap);
+        prefetch_tensormap(&a.bsmap);
+    }
     pdl_wait();
     if (warp == 1) {
         tmem_alloc2(tmem_slot, 512);
@@ -162,6 +169,8 @@ mx4_pair_kernel(const __grid_constant__ PairArgs a) {
     }
     tc_fence_before();
     __syncthreads();
+    // only with its tensor memory in hand does this kernel let the next one start
+    if (threadIdx.x == 0) pdl_launch_dependents();
     cluster_arrive();                                                // barriers of both CTAs ready
     cluster_wait();
     tc_fence_after();
@@ -187,11 +196,11 @@ mx4_pair_kernel(const __grid_constant__ PairArgs a) {
                 if (elect_one()) {
                     uint8_t *sA = smem + st * C::kStage, *sB = sA + C::kA, *sfA = sB + C::kB, *sfB = sfA + C::kSfA;
                     const uint32_t bar = full0 + 8u * (uint32_t)st;
-                    if (rank == 0) mbar_expect_tx(full + st, 2 * C::kStage);
+                    if (rank == 0) mbar_expect_tx(full + st, 2 * (C::kA + (uint32_t)a.bn * 64u + C::kSfA + C::kSfB));
                     tma_load_2d_pair(sA, &a.amap, kt * 128, ta * 256 + rank * 128, bar);
-                    tma_load_2d_pair(sB, &a.bmap, kt * 128, tb * BN + rank * (BN / 2), bar);
+                    tma_load_2d_pair(sB, &a.bmap, kt * 128, tb * a.bn + rank * (a.bn / 2), bar);
                     tma_load_2d_pair(sfA, &a.asmap, kt * 256, ta * 2 + rank, bar);
-                    tma_load_2d_pair(sfB, &a.bsmap, kt * 256, tb * C::kBands, bar);
+                    tma_load_2d_pair(sfB, &a.bsmap, kt * 256, S > 1 ? tb * C::kBands : tb * a.bn / 128, bar);
                 }
                 __syncwarp();
             }
@@ -207,6 +216,9 @@ mx4_pair_kernel(const __grid_constant__ PairArgs a) {
                 if (!(ok = __all_sync(0xFFFFFFFFu, ok))) break;
             }
             const uint32_t d = tmem + (it & 1 ? C::kD1 : 0u);
+            // first scale column of the tile's rows of B in its bands (rows form and
+            // S = 1: tiles start at multiples of 64; S > 1: each tile has its own bands)
+            const uint32_t b0 = S > 1 ? 0u : (uint32_t)((tile / a.Ta) * a.bn % 128) / 32u;
             for (int kt = 0; kt < a.KT; ++kt, ++i) {
                 const int st = i % kS;
                 ok = mbar_wait_abortable(full + st, (uint32_t)(i / kS) & 1u, flags);   // in both CTAs
@@ -217,6 +229,7 @@ mx4_pair_kernel(const __grid_constant__ PairArgs a) {
                     const uint32_t sA = smem_u32(smem + st * C::kStage), sB = sA + C::kA, sfA = sB + C::kB,
                                    sfB = sfA + C::kSfA;
                     const uint32_t tA = tmem + C::kSf + (uint32_t)st * C::kSfCols, tB = tA + 8;
+                    const uint32_t idesc = idesc_mxf4(256, S ? a.bn : BN, 0);
                     const uint64_t ad = smem_desc_sw128(sA), bd = smem_desc_sw128(sB);
                     const int steps = left >= kTileK ? 4 : (int)((left + 63) / 64);
                     // scales: four columns per 128 rows and group
@@ -231,8 +244,8 @@ mx4_pair_kernel(const __grid_constant__ PairArgs a) {
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
                         if (j < steps)
-                            mma_mxf4_pair(d, ad + 2 * j, bd + 2 * j, idesc_mxf4(256, BN, (j & 1) * 2),
-                                          tA + 4 * (j >> 1), tB + 4 * C::kBands * (j >> 1), kt + j > 0 ? 1u : 0u);
+                            mma_mxf4_pair(d, ad + 2 * j, bd + 2 * j, idesc + ((j & 1) ? kIdescSf2 : 0u), tA + 4 * (j >> 1),
+                                          tB + b0 + 4 * C::kBands * (j >> 1), kt + j > 0 ? 1u : 0u);
                     mma_commit_pair(empty + st);
                     if (kt == a.KT - 1) mma_commit_pair(dfull + (it & 1));
                     flags[2] = i + 1;
@@ -253,45 +266,28 @@ mx4_pair_kernel(const __grid_constant__ PairArgs a) {
             tc_fence_after();
             const uint32_t d = tmem + (it & 1 ? C::kD1 : 0u) + ((uint32_t)(32 * q) << 16);
             const int arow = ta * 256 + rank * 128 + 32 * q;         // first row of A of this warp
-            // the columns shared with the other accumulator first
-            constexpr int kChunks = BN / 128;
-            const int first = C::kLag == 1 && (it & 1) == 0 ? kChunks - 1 : 0;
+            auto drained = [&] {                                     // the accumulator (its shared half) is read
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_remote_weak(free0 + 8u * (uint32_t)(it & 1));
+            };
+            if constexpr (S == 0) {
+                // 128 columns at a time (64 where 128 do not divide them), with
+                // overlapping accumulators the shared half first
+                constexpr int kCols = BN % 128 ? 64 : 128, kChunks = BN / kCols;
+                const int first = C::kLag == 1 && (it & 1) == 0 ? kChunks - 1 : 0;
 #pragma unroll 1
-            for (int p = 0; p < kChunks; ++p) {
-                const int c128 = 128 * ((p + first) % kChunks);
-                uint32_t v128[128];
+                for (int p = 0; p < kChunks; ++p) {
+                    const int c0 = kCols * ((p + first) % kChunks);
+                    uint32_t v[kCols];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) tmem_ld32(d + c128 + 32 * e, v128 + 32 * e);
-                tmem_ld_wait();
-                if (p == (C::kLag == 1 ? 0 : kChunks - 1)) {
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_remote_weak(free0 + 8u * (uint32_t)(it & 1));
-                }
-#pragma unroll
-                for (int hf = 0; hf < 2; ++hf) {
-                const uint32_t *v = v128 + 64 * hf;
-                const int c = c128 + 64 * hf;
-                if constexpr (SLICES) {
-                    const int64_t n = arow + lane;
-                    const int m0 = (tb * BN + c) / kMxSlices;
-#pragma unroll
-                    for (int e = 0; e < 64 / kMxSlices; ++e) {
-                        float y = __uint_as_float(v[kMxSlices * e + kMxSlices - 1]);   // small slices first
-#pragma unroll
-                        for (int j = kMxSlices - 2; j >= 0; --j) y += __uint_as_float(v[kMxSlices * e + j]);
-                        if (n < a.N && m0 + e < a.M) {
-                            const int64_t at = (int64_t)(m0 + e) * a.ldy + n;
-                            if (a.out == MQ_BF16) static_cast<__nv_bfloat16 *>(a.Y)[at] = __float2bfloat16_rn(y);
-                            else if (a.out == MQ_F16) static_cast<__half *>(a.Y)[at] = __float2half_rn(y);
-                            else static_cast<float *>(a.Y)[at] = y;
-                        }
-                    }
-                } else {
-                    const int n0 = tb * BN + c;
+                    for (int e = 0; e < kCols / 32; ++e) tmem_ld32(d + c0 + 32 * e, v + 32 * e);
+                    tmem_ld_wait();
+                    if (p == (C::kLag == 1 ? 0 : kChunks - 1)) drained();
+                    const int n0 = tb * BN + c0;
                     if (a.out == MQ_F32) {
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
+                        for (int h = 0; h < kCols / 32; ++h, ++piece) {
                             uint32_t w[32];
 #pragma unroll
                             for (int e = 0; e < 32; ++e) w[e] = v[32 * h + e];
@@ -299,25 +295,54 @@ mx4_pair_kernel(const __grid_constant__ PairArgs a) {
                             if (lane == 0) bulk_wait_read<1>();      // the piece before the last has left
                             __syncwarp();
                             stage_row(s, lane, w);
-                            store_piece<4>(a, s, lane, arow, n0 + 32 * h);
-                            ++piece;
+                            store_piece(a, s, lane, arow, n0 + 32 * h);
                         }
                     } else {
-                        uint32_t w[32];
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            const float x = __uint_as_float(v[2 * e]), y = __uint_as_float(v[2 * e + 1]);
-                            w[e] = a.out == MQ_BF16 ? pack2<__nv_bfloat16>(x, y) : pack2<__half>(x, y);
+                        for (int h = 0; h < kCols / 64; ++h, ++piece) {
+                            uint32_t w[32];
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) {
+                                const float x = __uint_as_float(v[64 * h + 2 * e]),
+                                            y = __uint_as_float(v[64 * h + 2 * e + 1]);
+                                w[e] = a.out == MQ_BF16 ? pack2<__nv_bfloat16>(x, y) : pack2<__half>(x, y);
+                            }
+                            uint8_t *s = mystg + (piece & 1) * C::kStg;
+                            if (lane == 0) bulk_wait_read<1>();
+                            __syncwarp();
+                            stage_row(s, lane, w);
+                            store_piece(a, s, lane, arow, n0 + 64 * h);
                         }
-                        uint8_t *s = mystg + (piece & 1) * C::kStg;
-                        if (lane == 0) bulk_wait_read<1>();
-                        __syncwarp();
-                        stage_row(s, lane, w);
-                        store_piece<2>(a, s, lane, arow, n0);
-                        ++piece;
                     }
                 }
+            } else {
+                // eight rows of Y (32 with S = 1) at a time
+                constexpr int kRows = S == 1 ? 32 : 8, kCols = kRows * S;
+                const int64_t n = arow + lane;
+                const int rows = S == 1 ? a.bn : a.tpt, m0 = tb * rows, mend = a.M - m0 < rows ? a.M : m0 + rows;
+#pragma unroll 1
+                for (int c = 0; c * S < a.bn && m0 + c < mend; c += kRows) {
+                    uint32_t v[kCols];
+                    float y[kRows];
+                    if constexpr (kCols % 32 == 0) {
+#pragma unroll
+                        for (int e = 0; e < kCols / 32; ++e) tmem_ld32(d + c * S + 32 * e, v + 32 * e);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < kCols / 16; ++e) tmem_ld16(d + c * S + 16 * e, v + 16 * e);
+                    }
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int e = 0; e < kRows; ++e) {
+                        y[e] = __uint_as_float(v[S * e + S - 1]);    // small slices first
+#pragma unroll
+                        for (int j = S - 2; j >= 0; --j) y[e] += __uint_as_float(v[S * e + j]);
+                    }
+                    if (a.out == MQ_BF16) store_column<__nv_bfloat16>(a, m0 + c, mend, n, y);
+                    else if (a.out == MQ_F16) store_column<__half>(a, m0 + c, mend, n, y);
+                    else store_column<float>(a, m0 + c, mend, n, y);
                 }
+                drained();
             }
         }
         if (lane == 0) bulk_wait_all();                              // Y is written before the CTA ends
@@ -347,10 +372,10 @@ mx4_pair_kernel(const __grid_constant__ PairArgs a) {
 
 using PairFn = void (*)(PairArgs);
 
-template <int BN, bool SLICES>
+template <int BN, int S>
 cudaError_t pick(PairFn *fn, size_t *smem) {
     static std::atomic<uint64_t> done{0};
-    *fn = mx4_pair_kernel<BN, SLICES>;
+    *fn = mx4_pair_kernel<BN, S>;
     *smem = PairCfg<BN>::kSmem;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -362,20 +387,44 @@ cudaError_t pick(PairFn *fn, size_t *smem) {
     return e;
 }
 
+constexpr int kClusters = 74;                // two CTAs each, one an SM
+
+// Clocks of a product of Ta x Tb tiles with bn rows of B: rounds of tiles, each
+// KT stages of four MMAs (bn / 2 clocks, at least 75) and about 1500 at its ends.
+int64_t clocks(int64_t Ta, int64_t Tb, int bn, int64_t KT) {
+    return (Ta * Tb + kClusters - 1) / kClusters * (KT * 4 * (bn / 2 < 75 ? 75 : bn / 2) + 1500);
+}
+
 }  // namespace
 
-bool mx_pair_takes(const MxProduct &p) { return p.M * p.slices > 128; }
+bool mx_pair_takes(const MxProduct &p) { return p.slices != 1 ? p.slice.Tb > 0 : p.M > 128; }
+
+MxSlicing mx_slicing(int64_t M, int out) {
+    MxSlicing s{};
+    if (M * kMxSlices <= 128) {                  // one tile of the kernel for few rows
+        s.S = kMxSlices;
+        s.tpt = (int)M;
+        s.rows = M * kMxSlices;
+        s.bands = 1;
+        s.bn = (int)s.rows;
+        return s;
+    }
+    // Six slices leave at most 2^-16 of a block's largest value, far below half
+    // a step of a 16-bit output (2^-9, 2^-12), and take a quarter less of the
+    // tensor cores' time, which bounds this product; fp32 outputs keep eight.
+    s.S = out == MQ_F32 ? 8 : 6;
+    const int most = 192 / s.S;
+    s.Tb = (int)((M + most - 1) / most);
+    s.tpt = (int)((M + s.Tb - 1) / s.Tb);        // rows of X dealt evenly
+    s.bn = (s.tpt * s.S + 15) / 16 * 16;
+    s.rows = (int64_t)s.Tb * s.bn;
+    s.bands = (int64_t)s.Tb * 2;
+    return s;
+}
 
 mq_status launch_mx_pair(const MxProduct &p, cudaStream_t st) {
     const mq_mx4 *w = p.w;
-    const bool slices = p.slices > 1;
-    const int64_t cols = p.M * p.slices;
-    const int64_t ra = slices ? w->rows : cols, rb = slices ? cols : w->rows;
-    constexpr int BN = 256;
-    PairFn fn;
-    size_t smem;
-    cudaError_t e = slices ? pick<BN, true>(&fn, &smem) : pick<BN, false>(&fn, &smem);
-    if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
+    const int size = p.out == MQ_F32 ? 4 : 2;
     PairArgs a{};
     a.Y = p.Y;
     a.ldy = p.ldy;
@@ -384,21 +433,52 @@ mq_status launch_mx_pair(const MxProduct &p, cudaStream_t st) {
     a.K = w->K;
     a.KT = (int)((w->K + kTileK - 1) / kTileK);
     a.out = p.out;
-    const int64_t Ta = (ra + 255) / 256, Tb = (rb + BN - 1) / BN;
+    PairFn fn;
+    size_t smem;
+    cudaError_t e;
+    int64_t Ta, Tb;
+    bool maps;
+    // TMA stores want row strides in 16 bytes, and cut a box off at the tensor's
+    // edge in steps of 16 bytes only
+    if (p.slices == 1 && p.ldy * size % 16 == 0 && w->rows * size % 16 == 0) {
+        Ta = (p.M + 255) / 256;
+        a.bn = 256;
+        for (int bn : {192, 128})
+            if (clocks(Ta, (w->rows + bn - 1) / bn, bn, a.KT) < clocks(Ta, (w->rows + a.bn - 1) / a.bn, a.bn, a.KT)) a.bn = bn;
+        Tb = (w->rows + a.bn - 1) / a.bn;
+        e = a.bn == 256 ? pick<256, 0>(&fn, &smem) : a.bn == 192 ? pick<192, 0>(&fn, &smem) : pick<128, 0>(&fn, &smem);
+        maps = mx_encode_codes(&a.amap, p.xcodes, p.M, w->K, 128) && mx_encode_scales(&a.asmap, p.xscales, p.M, w->K, 1) &&
+               mx_encode_codes(&a.bmap, w->codes, w->rows, w->K, a.bn / 2) &&
+               mx_encode_scales(&a.bsmap, w->scales, w->rows, w->K, a.bn > 128 ? 2 : 1) &&
+               mx_encode_y(&a.ymap, p.Y, p.M, w->rows, p.ldy, p.out);
+    } else {
+        Ta = (w->rows + 255) / 256;
+        int64_t xrows = p.M, sfrows = p.M;
+        if (p.slices == 1) {
+            a.bn = 192;
+            for (int bn : {128, 64})
+                if (clocks(Ta, (p.M + bn - 1) / bn, bn, a.KT) < clocks(Ta, (p.M + a.bn - 1) / a.bn, a.bn, a.KT)) a.bn = bn;
+            Tb = (p.M + a.bn - 1) / a.bn;
+            e = pick<192, 1>(&fn, &smem);
+        } else {
+            a.bn = p.slice.bn;
+            a.tpt = p.slice.tpt;
+            Tb = p.slice.Tb;
+            xrows = p.slice.rows;
+            sfrows = p.slice.bands * 128;
+            e = p.slice.S == 6 ? pick<192, 6>(&fn, &smem) : pick<192, 8>(&fn, &smem);
+        }
+        maps = mx_encode_codes(&a.amap, w->codes, w->rows, w->K, 128) &&
+               mx_encode_scales(&a.asmap, w->scales, w->rows, w->K, 1) &&
+               mx_encode_codes(&a.bmap, p.xcodes, xrows, w->K, a.bn / 2) &&
+               mx_encode_scales(&a.bsmap, p.xscales, sfrows, w->K, 2);
+    }
+    if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
+    if (!maps) return fail(MQ_ERR_CUDA, "cuTensorMapEncodeTiled (MXFP4 product)");
     if (Ta * Tb > 0x3FFFFFFF) return fail(MQ_ERR_UNSUPPORTED, "too many output tiles");
     a.Ta = (int)Ta;
     a.Tb = (int)Tb;
-    // TMA stores want row strides in 16 bytes, and cut a box off at the tensor's
-    // edge in steps of 16 bytes only (columns behind an odd N were overwritten)
-    const int size = p.out == MQ_F32 ? 4 : 2;
-    a.tma_y = !slices && p.ldy * size % 16 == 0 && w->rows * size % 16 == 0;
-    if (!mx_encode_codes(&a.amap, slices ? w->codes : p.xcodes, ra, w->K, 128) ||
-        !mx_encode_codes(&a.bmap, slices ? p.xcodes : w->codes, rb, w->K, BN / 2) ||
-        !mx_encode_scales(&a.asmap, slices ? w->scales : p.xscales, ra, w->K, 1) ||
-        !mx_encode_scales(&a.bsmap, slices ? p.xscales : w->scales, rb, w->K, BN / 128) ||
-        (a.tma_y && !mx_encode_y(&a.ymap, p.Y, p.M, w->rows, p.ldy, p.out)))
-        return fail(MQ_ERR_CUDA, "cuTensorMapEncodeTiled (MXFP4 product)");
-    int64_t clusters = Ta * Tb < 74 ? Ta * Tb : 74;
+    const int64_t clusters = Ta * Tb < kClusters ? Ta * Tb : kClusters;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;

@@ -482,6 +482,8 @@ __host__ __device__ constexpr uint32_t idesc_mxf4(int M, int N, int id) {
          | ((uint32_t)id << 29);          // A scale bytes
 }
 
+constexpr uint32_t kIdescSf2 = (2u << 4) | (2u << 29);   // added to idesc_mxf4(.., 0): the other two bytes
+
 // Byte offset of 16-byte chunk `c` (0..7) of row `row` inside a 128-byte
 // swizzled K-major tile whose rows are 128 bytes.
 __host__ __device__ __forceinline__ uint32_t sw128_offset(uint32_t row, uint32_t c) {
