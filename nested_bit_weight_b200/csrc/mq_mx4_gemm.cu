@@ -63,9 +63,9 @@ __device__ int g_test_drop_mx4;
 
 template <int BN>
 struct MxCfg {
-    static constexpr int kBands = BN > 128 ? 2 : 1;                 // 128-row bands of the N operand
+    static_assert(BN <= 128, "one row band of scales");
     static constexpr uint32_t kA = kTileN * 128, kB = BN * 128;     // codes of a stage
-    static constexpr uint32_t kSfA = 1024, kSfB = 1024 * kBands;    // scales of a stage
+    static constexpr uint32_t kSfA = 1024, kSfB = 1024;    // scales of a stage
     static constexpr uint32_t kStage = kA + kB + kSfA + kSfB;       // a multiple of 1024
     // parts sent to this CTA: [CTA][owned columns / 4][128][4] fp32, at least four
     // columns for each of eight CTAs
@@ -74,8 +74,8 @@ struct MxCfg {
     static constexpr int kPerSm = BN <= 32 ? 2 : 1;
     static constexpr int kRoom = (kPerSm == 2 ? 113 : 226) * 1024 - 2048 - (int)kParts;
     static constexpr int kStages = kRoom / (int)kStage < 6 ? kRoom / (int)kStage : 6;
-    static constexpr uint32_t kSfCols = 8 + 8 * kBands;             // TMEM columns of a stage's scales
-    static constexpr uint32_t kD = 0, kSf = BN < 32 ? 32 : BN;      // TMEM: accumulator, then scales
+    static constexpr uint32_t kSfCols = 16;           // TMEM columns of a stage's scales
+    static constexpr uint32_t kSf = BN < 32 ? 32 : BN;              // TMEM: accumulator, then scales
     static constexpr uint32_t kCols = kSf + kStages * kSfCols <= 256 ? 256 : 512;
     static_assert(kSf + kStages * kSfCols <= kCols, "TMEM columns");
     // With one row of X the four slicing warps are on four stages at once: in a
@@ -97,7 +97,7 @@ struct MxArgs {
     int64_t ldy;
     int M, N;                      // rows of X before slicing, output features
     int64_t K, G;                  // columns, 128-column groups
-    int MB, KT, CS;                // X tiles, K tiles, CTAs per output tile
+    int KT, CS;                    // K tiles, CTAs per output tile
     int lper;                      // log2 of the columns a CTA of a cluster adds up, at least 2
     int slices;                    // 1, or kMxSlices columns of D per row of X
     int out;                       // type of Y
@@ -119,10 +119,10 @@ __device__ __forceinline__ __half to<__half>(float v) { return __float2half_rn(v
 template <>
 __device__ __forceinline__ __nv_bfloat16 to<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
-// Four columns m0 .. m0 + 3 (those below M) of feature n to Y.
+// Rows m0 .. m0 + 3 (those below M) of feature n to Y.
 template <class T>
-__device__ __forceinline__ void store4(const MxArgs &a, int64_t m0, int64_t n, const float (&y)[4]) {
-    T *dst = static_cast<T *>(a.Y) + m0 * a.ldy + n;
+__device__ __forceinline__ void store4(const MxArgs &a, int m0, int64_t n, const float (&y)[4]) {
+    T *dst = static_cast<T *>(a.Y) + (int64_t)m0 * a.ldy + n;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         if (m0 + e < a.M) *dst = to<T>(y[e]);
@@ -167,20 +167,20 @@ __device__ __forceinline__ void read_columns(uint32_t base, int slices, int live
 // CTAs that own the columns, which then add what they were sent.
 template <int BN, class T>
 __device__ __forceinline__ void epilogue(const MxArgs &a, uint32_t base, float *parts, uint64_t *sent, int rank,
-                                         int live, int64_t m0, int64_t n, int row, bool ok, volatile int *flags) {
+                                         int64_t n, int row, bool ok, volatile int *flags) {
     if (a.CS == 1) {
         if (ok)
-            read_columns<BN>(base, a.slices, live, [&](int col, const float (&y)[4]) {
-                if (n < a.N) store4<T>(a, m0 + col, n, y);
+            read_columns<BN>(base, a.slices, a.M, [&](int col, const float (&y)[4]) {
+                if (n < a.N) store4<T>(a, col, n, y);
             });
         return;
     }
-    const int lper = a.lper, first = rank << lper, left = live - first, per = 1 << lper;
+    const int lper = a.lper, first = rank << lper, left = a.M - first, per = 1 << lper;
     const int groups = ((left < per ? left : per) + 3) / 4;   // of four columns owned; <= 0: none
     float4 *const p4 = reinterpret_cast<float4 *>(parts);     // [CTA][group][row]
     if (ok) {
         const uint32_t to0 = smem_u32(p4 + ((size_t)rank << (lper - 2)) * kTileN + row), bar0 = smem_u32(sent);
-        read_columns<BN>(base, a.slices, live, [&](int col, const float (&y)[4]) {
+        read_columns<BN>(base, a.slices, a.M, [&](int col, const float (&y)[4]) {
             const uint32_t owner = (uint32_t)(col >> lper), at = to0 + (uint32_t)((col & (per - 1)) >> 2) * (kTileN * 16);
             st_async_v4(cluster_map(at, owner), y[0], y[1], y[2], y[3], cluster_map(bar0, owner));
         });
@@ -201,7 +201,7 @@ __device__ __forceinline__ void epilogue(const MxArgs &a, uint32_t base, float *
             y[2] += z.z;
             y[3] += z.w;
         }
-        if (n < a.N) store4<T>(a, m0 + first + 4 * g, n, y);
+        if (n < a.N) store4<T>(a, first + 4 * g, n, y);
     }
 }
 
@@ -215,12 +215,12 @@ mx4_gemm_kernel(const __grid_constant__ MxArgs a) {
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     float *parts = reinterpret_cast<float *>(smem + kS * C::kStage);
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + kS * C::kStage + C::kParts), *empty = full + kS, *done = empty + kS, *sent = done + 1;
-    volatile int *flags = reinterpret_cast<volatile int *>(sent + 1);   // [0] abort [1] loads [2] MMA stages
+    volatile int *flags = reinterpret_cast<volatile int *>(sent + 1);   // [0] abort [1] loads
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sent + 1) + 4;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = a.CS > 1 ? (int)(blockIdx.x % a.CS) : 0;
-    const int tile = (int)(blockIdx.x / a.CS), t = tile / a.MB, mb = tile % a.MB;
+    const int t = (int)(blockIdx.x / a.CS);      // tile: 128 features, all rows of X
     const int k0 = (int)((int64_t)rank * a.KT / a.CS), k1 = (int)((int64_t)(rank + 1) * a.KT / a.CS);
 
     if (threadIdx.x == 0) {
@@ -232,7 +232,7 @@ mx4_gemm_kernel(const __grid_constant__ MxArgs a) {
         }
         mbar_init(done, 1);
         mbar_init(sent, 1);
-        flags[0] = flags[1] = flags[2] = 0;
+        flags[0] = flags[1] = 0;
         fence_mbar_init();
     }
     __syncthreads();
@@ -243,8 +243,6 @@ mx4_gemm_kernel(const __grid_constant__ MxArgs a) {
 
     if (warp == 0) {
         // -------------------------------------------------------------- loads
-        const int64_t xband = (int64_t)mb * BN / 128, xbands = ((int64_t)a.M * a.slices + 127) / 128;
-        const int bands = xbands - xband < C::kBands ? (int)(xbands - xband) : C::kBands;
         for (int i = 0; i < k1 - k0; ++i) {
             const int st = i % kS, kt = k0 + i;
 #ifdef MQ_TEST_HOOKS
@@ -258,13 +256,12 @@ mx4_gemm_kernel(const __grid_constant__ MxArgs a) {
             if (elect_one()) {
                 uint8_t *sA = smem + st * C::kStage, *sB = sA + C::kA, *sfA = sB + C::kB, *sfB = sfA + C::kSfA;
                 const uint32_t sfbytes = 512u * (uint32_t)(a.G - 2 * kt < 2 ? a.G - 2 * kt : 2);
-                mbar_expect_tx(full + st, C::kA + sfbytes + (FUSED ? 0u : C::kB + sfbytes * bands));
+                mbar_expect_tx(full + st, C::kA + sfbytes + (FUSED ? 0u : C::kB + sfbytes));
                 tma_load_2d(sA, &a.wmap, kt * 128, t * kTileN, full + st);
                 bulk_g2s(sfA, a.ws + ((int64_t)t * a.G + 2 * kt) * 512, sfbytes, full + st);
                 if constexpr (!FUSED) {
-                    tma_load_2d(sB, &a.xmap, kt * 128, mb * BN, full + st);
-                    for (int b = 0; b < bands; ++b)
-                        bulk_g2s(sfB + b * 1024, a.xs + ((xband + b) * a.G + 2 * kt) * 512, sfbytes, full + st);
+                    tma_load_2d(sB, &a.xmap, kt * 128, 0, full + st);
+                    bulk_g2s(sfB, a.xs + 2 * (int64_t)kt * 512, sfbytes, full + st);   // rows of X: one band
                 }
                 flags[1] = i + 1;
             }
@@ -279,38 +276,47 @@ mx4_gemm_kernel(const __grid_constant__ MxArgs a) {
         pdl_launch_dependents();
         named_arrive(1, 160);                    // the epilogue may read the address
         const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(tmem_slot);
-        for (int i = 0; i < k1 - k0; ++i) {
-            const int st = i % kS;
-            const bool ok = mbar_wait_abortable(full + st, (uint32_t)(i / kS) & 1u, flags);
+        // what does not change is worked out before the loop, and the ring's slot
+        // and phase are counted: see the pair product
+        uint32_t st = 0, phase = 0;
+        const uint32_t s0 = smem_u32(smem);
+        const uint64_t ad0 = smem_desc_sw128(s0), bd0 = smem_desc_sw128(s0 + C::kA),
+                       sa0 = smem_desc_sf(s0 + C::kA + C::kB), sb0 = smem_desc_sf(s0 + C::kA + C::kB + C::kSfA);
+        const uint32_t idesc = idesc_mxf4(kTileN, BN, 0);
+        const int64_t left = a.K - (int64_t)(k1 - 1) * kTileK;
+        const int tail = left >= kTileK ? 4 : (int)((left + 63) / 64);   // MMAs of the last stage
+        int i = 0;
+        for (; i < k1 - k0; ++i) {
+            const bool ok = mbar_wait_abortable(full + st, phase, flags);
             if (!__all_sync(0xFFFFFFFFu, ok)) break;
             tc_fence_after();
-            const int64_t left = a.K - (int64_t)(k0 + i) * kTileK;
             if (elect_one()) {
-                const uint32_t sA = smem_u32(smem + st * C::kStage), sB = sA + C::kA, sfA = sB + C::kB,
-                               sfB = sfA + C::kSfA;
+                const uint64_t step = (uint64_t)st * (C::kStage >> 4);
                 const uint32_t tA = tmem + C::kSf + st * C::kSfCols, tB = tA + 8;
-                const uint64_t ad = smem_desc_sw128(sA), bd = smem_desc_sw128(sB);
-                const int steps = left >= kTileK ? 4 : (int)((left + 63) / 64);
+                const int steps = i + 1 < k1 - k0 ? 4 : tail;
                 // scales: four columns per 128 rows and group
-#pragma unroll
-                for (int g = 0; g < 2; ++g)
-                    if (2 * g < steps) {
-                        tmem_cp_sf(tA + 4 * g, smem_desc_sf(sfA + 512 * g));
-#pragma unroll
-                        for (int b = 0; b < C::kBands; ++b)
-                            tmem_cp_sf(tB + 4 * (C::kBands * g + b), smem_desc_sf(sfB + 1024 * b + 512 * g));
-                    }
+                tmem_cp_sf(tA, sa0 + step);
+                tmem_cp_sf(tB, sb0 + step);
+                if (steps > 2) {
+                    tmem_cp_sf(tA + 4, sa0 + step + 32);
+                    tmem_cp_sf(tB + 4, sb0 + step + 32);
+                }
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
                     if (j < steps)
-                        mma_mxf4(tmem + C::kD, ad + 2 * j, bd + 2 * j, idesc_mxf4(kTileN, BN, (j & 1) * 2),
-                                 tA + 4 * (j >> 1), tB + 4 * C::kBands * (j >> 1), i + j > 0 ? 1u : 0u);
+                        mma_mxf4(tmem, ad0 + step + 2 * j, bd0 + step + 2 * j, idesc + ((j & 1) ? kIdescSf2 : 0u),
+                                 tA + 4 * (j >> 1), tB + 4 * (j >> 1), i + j > 0 ? 1u : 0u);
                 mma_commit(empty + st);
                 if (i == k1 - k0 - 1) mma_commit(done);
-                flags[2] = i + 1;
             }
             __syncwarp();
+            if (++st == kS) {
+                st = 0;
+                phase ^= 1u;
+            }
         }
+        // MMAs in flight land (after a wait that gave up)
+        if (i > 0 && i < k1 - k0) mbar_wait_bounded(empty + (i - 1) % kS, (uint32_t)((i - 1) / kS) & 1u);
     }
     __syncwarp();
 
@@ -371,24 +377,21 @@ mx4_gemm_kernel(const __grid_constant__ MxArgs a) {
 
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3, row = 32 * q + lane;              // TMEM lane quarter of this warp
-    const int cols = BN / a.slices;                           // rows of X of this tile
-    const int64_t m0 = (int64_t)mb * cols;
-    const int live = a.M - m0 < cols ? (int)(a.M - m0) : cols;
     if (a.CS > 1) cluster_wait();
     if (warp >= kEpiW0) {
         if (a.CS > 1 && threadIdx.x == 32 * kEpiW0) {
-            const int left = live - (rank << a.lper), own = left < (1 << a.lper) ? left : 1 << a.lper;
+            const int left = a.M - (rank << a.lper), own = left < (1 << a.lper) ? left : 1 << a.lper;
             if (own > 0) mbar_expect_tx(sent, (uint32_t)a.CS * (uint32_t)((own + 3) / 4) * (kTileN * 16));
         }
         bool ok = mbar_wait_backoff(done, 0, flags);
         ok = __all_sync(0xFFFFFFFFu, ok);
         named_sync(1, 160);
         tc_fence_after();
-        const uint32_t base = *reinterpret_cast<volatile uint32_t *>(tmem_slot) + C::kD + ((uint32_t)(32 * q) << 16);
+        const uint32_t base = *reinterpret_cast<volatile uint32_t *>(tmem_slot) + ((uint32_t)(32 * q) << 16);
         const int64_t n = (int64_t)t * kTileN + row;
-        if (a.out == MQ_BF16) epilogue<BN, __nv_bfloat16>(a, base, parts, sent, rank, live, m0, n, row, ok, flags);
-        else if (a.out == MQ_F16) epilogue<BN, __half>(a, base, parts, sent, rank, live, m0, n, row, ok, flags);
-        else epilogue<BN, float>(a, base, parts, sent, rank, live, m0, n, row, ok, flags);
+        if (a.out == MQ_BF16) epilogue<BN, __nv_bfloat16>(a, base, parts, sent, rank, n, row, ok, flags);
+        else if (a.out == MQ_F16) epilogue<BN, __half>(a, base, parts, sent, rank, n, row, ok, flags);
+        else epilogue<BN, float>(a, base, parts, sent, rank, n, row, ok, flags);
         tc_fence_before();
     }
 
@@ -398,8 +401,6 @@ mx4_gemm_kernel(const __grid_constant__ MxArgs a) {
         atomicOr(&g_mx_timeout, 1u);
         for (int s = 0; s < kS && s < flags[1]; ++s)
             mbar_wait_bounded(full + s, (uint32_t)((flags[1] - 1 - s) / kS) & 1u);
-        for (int s = 0; s < kS && s < flags[2]; ++s)
-            mbar_wait_bounded(empty + s, (uint32_t)((flags[2] - 1 - s) / kS) & 1u);
     }
     tc_fence_before();
     __syncthreads();
@@ -454,11 +455,10 @@ mq_status launch(const MxProduct &p, cudaStream_t st) {
     a.N = (int)w->rows;
     a.K = w->K;
     a.G = mx_groups(w->K);
-    a.MB = (int)((cols + BN - 1) / BN);
     a.KT = (int)((w->K + kTileK - 1) / kTileK);
     a.slices = p.slices;
     a.out = p.out;
-    const int64_t tiles = (w->rows + kTileN - 1) / kTileN * a.MB;
+    const int64_t tiles = (w->rows + kTileN - 1) / kTileN;
     // K is split while the CTAs still fit the GPU once (kPerSm an SM) and each keeps kMinStages of K (two
     // stages each: 7.2 us for 16 x 4096 x 4096, four: 5.3, six: 6.4)
     a.CS = 1;

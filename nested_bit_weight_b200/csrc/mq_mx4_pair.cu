@@ -134,7 +134,7 @@ mx4_pair_kernel(const __grid_constant__ PairArgs a) {
     uint8_t *stg = smem + kS * C::kStage;                            // [warp][2][4096]
     uint64_t *full = reinterpret_cast<uint64_t *>(stg + 8 * C::kStg);
     uint64_t *empty = full + kS, *dfull = empty + kS, *dfree = dfull + 2;
-    volatile int *flags = reinterpret_cast<volatile int *>(dfree + 2);   // [0] abort [2] MMA stages
+    volatile int *flags = reinterpret_cast<volatile int *>(dfree + 2);   // [0] abort
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(dfree + 2) + 4;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -150,7 +150,7 @@ mx4_pair_kernel(const __grid_constant__ PairArgs a) {
             mbar_init(dfull + i, 1);
             mbar_init(dfree + i, 8);                                 // four epilogue warps of each CTA
         }
-        flags[0] = flags[2] = 0;
+        flags[0] = 0;
         fence_mbar_init();
     }
     if (threadIdx.x == 0) {
@@ -207,8 +207,17 @@ mx4_pair_kernel(const __grid_constant__ PairArgs a) {
         }
     } else if (warp == 1 && rank == 0) {
         // --------------------------------------------------------------- MMAs
-        int i = 0, it = 0;
+        // everything that does not change is worked out before the loop, and the
+        // ring's slot and phase are counted, not divided for: what this warp does
+        // between a stage's MMAs and the next is time the tensor core idles
+        int it = 0, last = -1;                                       // last slot committed
+        uint32_t st = 0, phase = 0, lastphase = 0;
         bool ok = true;
+        const uint32_t s0 = smem_u32(smem);
+        const uint64_t ad0 = smem_desc_sw128(s0), bd0 = smem_desc_sw128(s0 + C::kA),
+                       sa0 = smem_desc_sf(s0 + C::kA + C::kB), sb0 = smem_desc_sf(s0 + C::kA + C::kB + C::kSfA);
+        const uint32_t idesc = idesc_mxf4(256, S ? a.bn : BN, 0);
+        const int tail = (int)((a.K - (int64_t)(a.KT - 1) * kTileK + 63) / 64);   // MMAs of the last stage of a tile
         for (int tile = cluster; tile < tiles && ok; tile += nclusters, ++it) {
             if (it >= C::kLag) {
                 const int w = it - C::kLag;
@@ -219,40 +228,41 @@ mx4_pair_kernel(const __grid_constant__ PairArgs a) {
             // first scale column of the tile's rows of B in its bands (rows form and
             // S = 1: tiles start at multiples of 64; S > 1: each tile has its own bands)
             const uint32_t b0 = S > 1 ? 0u : (uint32_t)((tile / a.Ta) * a.bn % 128) / 32u;
-            for (int kt = 0; kt < a.KT; ++kt, ++i) {
-                const int st = i % kS;
-                ok = mbar_wait_abortable(full + st, (uint32_t)(i / kS) & 1u, flags);   // in both CTAs
+            for (int kt = 0; kt < a.KT; ++kt) {
+                ok = mbar_wait_abortable(full + st, phase, flags);   // in both CTAs
                 if (!(ok = __all_sync(0xFFFFFFFFu, ok))) break;
                 tc_fence_after();
-                const int64_t left = a.K - (int64_t)kt * kTileK;
                 if (elect_one()) {
-                    const uint32_t sA = smem_u32(smem + st * C::kStage), sB = sA + C::kA, sfA = sB + C::kB,
-                                   sfB = sfA + C::kSfA;
-                    const uint32_t tA = tmem + C::kSf + (uint32_t)st * C::kSfCols, tB = tA + 8;
-                    const uint32_t idesc = idesc_mxf4(256, S ? a.bn : BN, 0);
-                    const uint64_t ad = smem_desc_sw128(sA), bd = smem_desc_sw128(sB);
-                    const int steps = left >= kTileK ? 4 : (int)((left + 63) / 64);
+                    const uint64_t step = (uint64_t)st * (C::kStage >> 4);
+                    const uint32_t tA = tmem + C::kSf + st * C::kSfCols, tB = tA + 8;
+                    const int steps = kt + 1 < a.KT ? 4 : tail;
                     // scales: four columns per 128 rows and group
 #pragma unroll
                     for (int g = 0; g < 2; ++g)
                         if (2 * g < steps) {
-                            tmem_cp_sf_pair(tA + 4 * g, smem_desc_sf(sfA + 512 * g));
+                            tmem_cp_sf_pair(tA + 4 * g, sa0 + step + 32 * g);
 #pragma unroll
                             for (int b = 0; b < C::kBands; ++b)
-                                tmem_cp_sf_pair(tB + 4 * (C::kBands * g + b), smem_desc_sf(sfB + 1024 * b + 512 * g));
+                                tmem_cp_sf_pair(tB + 4 * (C::kBands * g + b), sb0 + step + 64 * b + 32 * g);
                         }
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
                         if (j < steps)
-                            mma_mxf4_pair(d, ad + 2 * j, bd + 2 * j, idesc + ((j & 1) ? kIdescSf2 : 0u), tA + 4 * (j >> 1),
-                                          tB + b0 + 4 * C::kBands * (j >> 1), kt + j > 0 ? 1u : 0u);
+                            mma_mxf4_pair(d, ad0 + step + 2 * j, bd0 + step + 2 * j, idesc + ((j & 1) ? kIdescSf2 : 0u),
+                                          tA + 4 * (j >> 1), tB + b0 + 4 * C::kBands * (j >> 1), kt + j > 0 ? 1u : 0u);
                     mma_commit_pair(empty + st);
                     if (kt == a.KT - 1) mma_commit_pair(dfull + (it & 1));
-                    flags[2] = i + 1;
                 }
                 __syncwarp();
+                last = (int)st;
+                lastphase = phase;
+                if (++st == kS) {
+                    st = 0;
+                    phase ^= 1u;
+                }
             }
         }
+        if (!ok && last >= 0) mbar_wait_bounded(empty + last, lastphase);   // MMAs in flight land
     } else if (warp >= kEpiW0) {
         // ------------------------------------------------------------ epilogue
         const int q = warp & 3;                                      // TMEM lane quarter
@@ -357,8 +367,6 @@ mx4_pair_kernel(const __grid_constant__ PairArgs a) {
         // loads are given a millisecond (a load takes microseconds) to land
         const uint64_t t0 = global_ns();
         while (global_ns() - t0 < 1000000ull) __nanosleep(1000);
-        for (int s = 0; s < kS && s < flags[2]; ++s)
-            mbar_wait_bounded(empty + s, (uint32_t)((flags[2] - 1 - s) / kS) & 1u);
     }
     tc_fence_before();
     __syncthreads();
