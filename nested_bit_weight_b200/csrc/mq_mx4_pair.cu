@@ -133,9 +133,9 @@ mx4_pair_kernel(const __grid_constant__ PairArgs a) {
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint8_t *stg = smem + kS * C::kStage;                            // [warp][2][4096]
     uint64_t *full = reinterpret_cast<uint64_t *>(stg + 8 * C::kStg);
-    uint64_t *empty = full + kS, *dfull = empty + kS, *dfree = dfull + 2;
-    volatile int *flags = reinterpret_cast<volatile int *>(dfree + 2);   // [0] abort
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(dfree + 2) + 4;
+    uint64_t *empty = full + kS, *dfull = empty + kS, *dfree = dfull + 2, *ready = dfree + 2;
+    volatile int *flags = reinterpret_cast<volatile int *>(ready + 1);   // [0] abort
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(ready + 1) + 4;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = (int)(blockIdx.x & 1), cluster = (int)(blockIdx.x >> 1), nclusters = (int)(gridDim.x >> 1);
@@ -150,6 +150,7 @@ mx4_pair_kernel(const __grid_constant__ PairArgs a) {
             mbar_init(dfull + i, 1);
             mbar_init(dfree + i, 8);                                 // four epilogue warps of each CTA
         }
+        mbar_init(ready, 1);
         flags[0] = 0;
         fence_mbar_init();
     }
@@ -162,19 +163,10 @@ mx4_pair_kernel(const __grid_constant__ PairArgs a) {
         prefetch_tensormap(&a.asmap);
         prefetch_tensormap(&a.bsmap);
     }
-    pdl_wait();
-    if (warp == 1) {
-        tmem_alloc2(tmem_slot, 512);
-        tmem_relinquish2();
-    }
-    tc_fence_before();
     __syncthreads();
-    // only with its tensor memory in hand does this kernel let the next one start
-    if (threadIdx.x == 0) pdl_launch_dependents();
     cluster_arrive();                                                // barriers of both CTAs ready
     cluster_wait();
-    tc_fence_after();
-    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(tmem_slot);
+    pdl_wait();
 
     if (warp == 0) {
         // -------------------------------------------------------------- loads
@@ -205,14 +197,27 @@ mx4_pair_kernel(const __grid_constant__ PairArgs a) {
                 __syncwarp();
             }
         }
-    } else if (warp == 1 && rank == 0) {
+    } else if (warp == 1) {
         // --------------------------------------------------------------- MMAs
+        // tensor memory is taken after the previous kernel, so that it never waits
+        // for columns held here, and only with it in hand does this kernel let the
+        // next one start
+        tmem_alloc2(tmem_slot, 512);
+        tmem_relinquish2();
+        pdl_launch_dependents();
+        named_arrive(1, 160);                                        // the epilogue may read the address
+        if (rank == 1) {
+            if (lane == 0) mbar_arrive_remote_weak(cluster_map(smem_u32(ready), 0));
+        }
+        __syncwarp();
+        const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(tmem_slot);
         // everything that does not change is worked out before the loop, and the
         // ring's slot and phase are counted, not divided for: what this warp does
         // between a stage's MMAs and the next is time the tensor core idles
         int it = 0, last = -1;                                       // last slot committed
         uint32_t st = 0, phase = 0, lastphase = 0;
-        bool ok = true;
+        bool ok = rank == 0 && mbar_wait_abortable(ready, 0, flags); // the odd CTA has its columns too
+        ok = __all_sync(0xFFFFFFFFu, ok);                            // its warp has nothing more to do
         const uint32_t s0 = smem_u32(smem);
         const uint64_t ad0 = smem_desc_sw128(s0), bd0 = smem_desc_sw128(s0 + C::kA),
                        sa0 = smem_desc_sf(s0 + C::kA + C::kB), sb0 = smem_desc_sf(s0 + C::kA + C::kB + C::kSfA);
@@ -266,6 +271,9 @@ mx4_pair_kernel(const __grid_constant__ PairArgs a) {
     } else if (warp >= kEpiW0) {
         // ------------------------------------------------------------ epilogue
         const int q = warp & 3;                                      // TMEM lane quarter
+        named_sync(1, 160);
+        tc_fence_after();
+        const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(tmem_slot);
         uint8_t *mystg = stg + (warp - kEpiW0) * 2 * C::kStg;
         const uint32_t free0 = cluster_map(smem_u32(dfree), 0);
         int it = 0, piece = 0;
@@ -374,7 +382,7 @@ mx4_pair_kernel(const __grid_constant__ PairArgs a) {
     cluster_wait();
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc2(tmem, 512);
+        tmem_dealloc2(*reinterpret_cast<volatile uint32_t *>(tmem_slot), 512);
     }
 }
 
