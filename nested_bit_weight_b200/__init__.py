@@ -401,21 +401,30 @@ def mq_mx4_gemm_bf16_workspace_bytes(M: int, N: int, K: int) -> int:
     return lib.mq_mx4_gemm_bf16_workspace_bytes(M, N, K)
 
 
-_types: dict = {}          # torch dtype -> (MQ_* code, bytes); filled on first use (torch loads late)
+# Small calls are bound by the host, so the common case of each function below
+# (tensors on the current device, its current stream) takes no detours: torch's
+# names are looked up once, and no context is entered.
+_torch = _empty = _u8 = _raw_stream = _get_device = None
+_types: dict = {}          # torch dtype -> MQ_* code
+
+
+def _init() -> None:
+    global _torch, _empty, _u8, _raw_stream, _get_device
+    import torch
+    _types.update({torch.bfloat16: BF16, torch.float16: F16, torch.float32: F32})
+    _raw_stream, _get_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+    _torch, _empty, _u8 = torch, torch.empty, torch.uint8
 
 
 def _dtype_code(dtype) -> int:
-    if not _types:
-        import torch
-        _types.update({torch.bfloat16: (BF16, 2), torch.float16: (F16, 2), torch.float32: (F32, 4)})
     t = _types.get(dtype)
     if t is None:
         raise ValueError(f"dtype {dtype} is not one of bfloat16, float16, float32")
-    return t[0]
+    return t
 
 
-def _rows(t, what: str, cols: int | None = None, rows: int | None = None) -> int:
-    """Check a 2-D device tensor whose rows are contiguous; its row stride."""
+def _rows(t, what: str):
+    """Check a 2-D device tensor whose rows are contiguous: rows, columns, row stride."""
     try:
         n, k = t.shape
         ld, one = t.stride()
@@ -424,14 +433,22 @@ def _rows(t, what: str, cols: int | None = None, rows: int | None = None) -> int
         raise ValueError(f"{what} must be a 2-D tensor") from None
     if not cuda:
         raise ValueError(f"{what} must be on a GPU")
-    if (cols is not None and k != cols) or (rows is not None and n != rows):
-        raise ValueError(f"{what} has shape {(n, k)}, expected {(rows, cols)}")
     if one != 1 and k > 1:
         raise ValueError(f"{what} must have contiguous rows (stride 1 along the last axis)")
     if n <= 1:
-        return k or 1
+        return n, k, k or 1
     if ld < k:
         raise ValueError(f"the rows of {what} overlap")
+    return n, k, ld
+
+
+def _given(t, what: str, rows: int, cols: int, dtype, device) -> int:
+    """Check a tensor given for a result; its row stride."""
+    n, k, ld = _rows(t, what)
+    if (n, k) != (rows, cols):
+        raise ValueError(f"{what} has shape {(n, k)}, expected {(rows, cols)}")
+    if t.dtype != dtype or t.device != device:
+        raise ValueError(f"{what} differs in dtype or device")
     return ld
 
 
@@ -440,7 +457,7 @@ class _On:
     a call allocates belongs to the stream it runs on."""
 
     def __init__(self, device, stream):
-        import torch
+        torch = _torch
         if stream is None:
             stream = torch.cuda.current_stream(device)
         elif not isinstance(stream, torch.cuda.Stream):
@@ -459,71 +476,58 @@ class _On:
         return self._ctx.__exit__(*exc)
 
 
-class _Here:
-    """The common case of _On, without its cost (half the host time of a small
-    call): the current stream of the current device, nothing to switch."""
-
-    def __enter__(self):
-        return _raw_stream(self.index)
-
-    def __exit__(self, *exc):
-        return None
-
-
-_here = None
-_raw_stream = _get_device = None
-
-
-def _on(device, stream):
-    global _here, _raw_stream, _get_device
-    if _here is None:
-        import torch
-        _raw_stream, _get_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
-        _here = {}
-    if stream is None and device.index == _get_device():
-        h = _here.get(device.index)
-        if h is None:
-            h = _Here()
-            h.index = device.index
-            _here[device.index] = h
-        return h
-    return _On(device, stream)
+def _call(fn, device, stream, *args):
+    """fn(*args, stream handle) with the device and stream of the call current."""
+    i = device.index
+    if stream is None and i == _get_device():
+        return fn(*args, _raw_stream(i))
+    with _On(device, stream) as st:
+        return fn(*args, st)
 
 
 class Mx4Matrix:
     """A rows x K matrix in MXFP4 (device tensors): codes uint8 [rows, K/2] and
     the scale blocks (mq_mx4 in include/mq.h)."""
 
-    __slots__ = ("rows", "K", "device", "struct", "_codes", "_scales", "_buf")
+    __slots__ = ("rows", "K", "device", "_ptrs", "_struct", "_codes", "_scales", "_buf")
 
     def __init__(self, codes, scales, rows: int, K: int):
-        import torch
+        if _torch is None:
+            _init()
         for t, n, what in ((codes, mq_mx4_code_bytes(rows, K), "codes"),
                            (scales, mq_mx4_scale_bytes(rows, K), "scales")):
-            if t.dtype != torch.uint8 or not t.is_cuda or not t.is_contiguous() or t.numel() != n:
+            if t.dtype != _torch.uint8 or not t.is_cuda or not t.is_contiguous() or t.numel() != n:
                 raise ValueError(f"{what} must be {n} contiguous uint8 on a GPU")
         if codes.device != scales.device:
             raise ValueError("codes and scales are on different devices")
         self.rows, self.K, self.device = rows, K, codes.device
-        self._codes, self._scales, self._buf = codes, scales, None
-        self.struct = MqMx4(codes.data_ptr(), scales.data_ptr(), rows, K)
+        self._codes, self._scales, self._buf, self._struct = codes, scales, None, None
+        self._ptrs = codes.data_ptr(), scales.data_ptr()
 
     @classmethod
     def empty(cls, rows: int, K: int, device):
         """Uninitialised buffers for a rows x K matrix."""
-        import torch
+        if _torch is None:
+            _init()
+        return cls._new(rows, K, lambda n, dtype: _empty(n, dtype=dtype, device=device))
+
+    @classmethod
+    def _new(cls, rows: int, K: int, empty):
         if rows < 0 or K < 32 or K % 32:
             raise ValueError("need rows >= 0 and K a positive multiple of 32")
         self = cls.__new__(cls)
         # one allocation: the codes (rows of 16-byte multiples), then the scale blocks
-        nc, ns = rows * (K // 2), (rows + 127) // 128 * ((K + 127) // 128) * 512
-        buf = torch.empty(nc + ns, dtype=torch.uint8, device=device)
+        nc = rows * (K >> 1)
+        self._buf = buf = empty(nc + ((rows + 127) >> 7) * ((K + 127) >> 7) * 512, dtype=_u8)
         ptr = buf.data_ptr()
+        self._ptrs = ptr, ptr + nc
         self.rows, self.K, self.device = rows, K, buf.device
-        self._codes = self._scales = None
-        self._buf = buf
-        self.struct = MqMx4(ptr, ptr + nc, rows, K)
+        self._codes = self._scales = self._struct = None
         return self
+
+    @property
+    def _like(self):
+        return self._codes if self._buf is None else self._buf
 
     @property
     def codes(self):
@@ -537,94 +541,128 @@ class Mx4Matrix:
             self._scales = self._buf[self.rows * (self.K // 2):]
         return self._scales
 
+    @property
+    def struct(self) -> MqMx4:
+        s = self._struct
+        if s is None:
+            s = self._struct = MqMx4(*self._ptrs, self.rows, self.K)
+        return s
 
-def _mx4_out(out, rows: int, K: int, device) -> Mx4Matrix:
+
+def _mx4_out(out, rows: int, K: int, like) -> Mx4Matrix:
+    """The matrix for a result: `out`, or new buffers on the device of `like`
+    (tensor.new_empty takes less of the host than torch.empty)."""
     if out is None:
-        return Mx4Matrix.empty(rows, K, device)
-    if (out.rows, out.K) != (rows, K) or out.device != device:
-        raise ValueError(f"out is {out.rows} x {out.K} on {out.device}, expected {rows} x {K} on {device}")
+        return Mx4Matrix._new(rows, K, like.new_empty)
+    if (out.rows, out.K) != (rows, K) or out.device != like.device:
+        raise ValueError(f"out is {out.rows} x {out.K} on {out.device}, expected {rows} x {K} on {like.device}")
+    return out
+
+
+def _quantize(X, dt, rows, K, ld, out, st):
+    out = _mx4_out(out, rows, K, X)
+    codes, scales = out._ptrs
+    s = lib.mq_mx4_quantize(X.data_ptr(), dt, rows, K, ld, codes, scales, st)
+    if s:
+        _check(s)
     return out
 
 
 def mx4_quantize(X, out: Mx4Matrix | None = None, stream=None) -> Mx4Matrix:
     """Rows of X (bf16, fp16 or fp32 [rows, K], K a multiple of 32) in MXFP4;
     `out` (of the same size) receives them in place of new buffers."""
-    ld = _rows(X, "X")
-    rows, K = X.shape
-    dt = _dtype_code(X.dtype)
-    device = X.device
-    with _on(device, stream) as st:
-        out = _mx4_out(out, rows, K, device)
-        s = out.struct
-        _check(lib.mq_mx4_quantize(X.data_ptr(), dt, rows, K, ld, s.codes, s.scales, st))
+    if _torch is None:
+        _init()
+    rows, K, ld = _rows(X, "X")
+    return _call(_quantize, X.device, stream, X, _dtype_code(X.dtype), rows, K, ld, out)
+
+
+def _from_nested(weights, r, out, st):
+    w = weights.view(r)
+    out = _mx4_out(out, w.N, w.K, weights.planes)
+    _check(lib.mq_mx4_from_nested(w, *out._ptrs, st))
     return out
 
 
 def mx4_from_nested(weights: NestedWeights, r: int, out: Mx4Matrix | None = None, stream=None) -> Mx4Matrix:
     """The r-bit model of a nested parent in MXFP4."""
-    w = weights.view(r)
-    device = weights.planes.device
-    with _on(device, stream) as st:
-        out = _mx4_out(out, weights.N, weights.K, device)
-        s = out.struct
-        _check(lib.mq_mx4_from_nested(w, s.codes, s.scales, st))
+    if _torch is None:
+        _init()
+    return _call(_from_nested, weights.planes.device, stream, weights, r, out)
+
+
+def _dequantize(m, dtype, out, st):
+    if out is None:
+        out, ld = m._like.new_empty((m.rows, m.K), dtype=dtype), m.K
+    else:
+        ld = _given(out, "out", m.rows, m.K, dtype, m.device)
+    s = lib.mq_mx4_dequantize(m.struct, out.data_ptr(), _dtype_code(dtype), ld, st)
+    if s:
+        _check(s)
     return out
 
 
 def mx4_dequantize(m: Mx4Matrix, dtype=None, out=None, stream=None):
     """The values m stands for, bf16 (default) or fp32; both hold them exactly."""
-    import torch
+    if _torch is None:
+        _init()
     if dtype is None:
-        dtype = out.dtype if out is not None else torch.bfloat16
-    dt = _dtype_code(dtype)
-    with _on(m.device, stream) as st:
-        if out is None:
-            out, ld = torch.empty((m.rows, m.K), dtype=dtype, device=m.device), m.K
-        else:
-            ld = _rows(out, "out", m.K, m.rows)
-            if out.dtype != dtype or out.device != m.device:
-                raise ValueError("out differs in dtype or device")
-        _check(lib.mq_mx4_dequantize(m.struct, out.data_ptr(), dt, ld, st))
-    return out
+        dtype = out.dtype if out is not None else _torch.bfloat16
+    return _call(_dequantize, m.device, stream, m, dtype, out)
 
 
 def _mx4_y(Y, M: int, w: Mx4Matrix, dtype):
-    import torch
-    if dtype is None:
-        dtype = Y.dtype if Y is not None else torch.bfloat16
-    dt = _dtype_code(dtype)
+    """The tensor for a product's result, its dtype's code and its row stride."""
     if Y is None:
-        return torch.empty((M, w.rows), dtype=dtype, device=w.device), dt, w.rows
-    ldy = _rows(Y, "Y", w.rows, M)
-    if Y.dtype != dtype or Y.device != w.device:
-        raise ValueError("Y differs in dtype or device")
-    return Y, dt, ldy
+        if dtype is None:
+            dtype = _torch.bfloat16
+        dt, N = _dtype_code(dtype), w.rows
+        return w._like.new_empty((M, N), dtype=dtype), dt, N
+    if dtype is None:
+        dtype = Y.dtype
+    dt = _dtype_code(dtype)
+    return Y, dt, _given(Y, "Y", M, w.rows, dtype, w.device)
+
+
+def _gemm4(X, w, Y, dtype, st):
+    Y, dt, ldy = _mx4_y(Y, X.rows, w, dtype)
+    s = lib.mq_mx4_gemm(X.struct, w.struct, Y.data_ptr(), dt, ldy, st)
+    if s:
+        _check(s)
+    return Y
 
 
 def mx4_gemm(X: Mx4Matrix, w: Mx4Matrix, Y=None, dtype=None, stream=None):
     """Y = X . w^T, both in MXFP4 (X: M x K, w: N x K); Y bf16 (default), fp16
     or fp32 [M, N]."""
-    if X.device != w.device:
+    device = w.device
+    if X.device != device:
         raise ValueError("X and w are on different devices")
-    with _on(w.device, stream) as st:
-        Y, dt, ldy = _mx4_y(Y, X.rows, w, dtype)
-        _check(lib.mq_mx4_gemm(X.struct, w.struct, Y.data_ptr(), dt, ldy, st))
+    return _call(_gemm4, device, stream, X, w, Y, dtype)
+
+
+def _gemm16(X, M, ldx, w, Y, dtype, st):
+    Y, dt, ldy = _mx4_y(Y, M, w, dtype)
+    # one or two rows need no workspace; it is this call's own, on its stream
+    need = mq_mx4_gemm_bf16_workspace_bytes(M, w.rows, w.K) if M > 2 else 0
+    ws = w._like.new_empty(need, dtype=_u8) if need else None
+    s = lib.mq_mx4_gemm_bf16(X.data_ptr(), M, ldx, w.struct, Y.data_ptr(), dt, ldy,
+                             ws.data_ptr() if need else None, need, st)
+    if s:
+        _check(s)
     return Y
 
 
 def mx4_gemm_bf16(X, w: Mx4Matrix, Y=None, dtype=None, stream=None):
     """Y = X . w^T with X in bf16 [M, K] as it is, w in MXFP4."""
-    import torch
-    ldx = _rows(X, "X", w.K)
-    if X.dtype != torch.bfloat16:
+    if _torch is None:
+        _init()
+    M, K, ldx = _rows(X, "X")
+    if K != w.K:
+        raise ValueError(f"X has {K} columns, expected {w.K}")
+    if X.dtype != _torch.bfloat16:
         raise ValueError("X must be bfloat16")
-    if X.device != w.device:
+    device = w.device
+    if X.device != device:
         raise ValueError("X and w are on different devices")
-    M = X.shape[0]
-    with _on(w.device, stream) as st:
-        Y, dt, ldy = _mx4_y(Y, M, w, dtype)
-        need = mq_mx4_gemm_bf16_workspace_bytes(M, w.rows, w.K)
-        ws = torch.empty(need, dtype=torch.uint8, device=w.device) if need else None
-        _check(lib.mq_mx4_gemm_bf16(X.data_ptr(), M, ldx, w.struct, Y.data_ptr(), dt, ldy,
-                                    ws.data_ptr() if ws is not None else None, need, st))
-    return Y
+    return _call(_gemm16, device, stream, X, M, ldx, w, Y, dtype)
