@@ -38,102 +38,125 @@ __device__ __forceinline__ uint32_t scaled_codes8(const float (&u)[8], float f) 
     return mx_codes8(v);
 }
 
-// Eight consecutive elements as loaded: one or two 16-byte words.  amax is the
-// largest magnitude of the block of 32 in this and the three adjacent lanes, as
-// fp32 bits; magnitudes are compared as integers, so that a NaN wins.
+// The larger magnitude of both halves (or of one number); a NaN wins, the signs
+// are left meaningless.
 template <int DT>
-struct Raw8 {
-    uint4 v;
-    static constexpr int kBytes = 2;
-    __device__ void load(const void *p) { v = __ldcs(reinterpret_cast<const uint4 *>(p)); }
-    __device__ void zero() { v = make_uint4(0u, 0u, 0u, 0u); }
-    __device__ uint32_t amax() const {
-        constexpr uint32_t kMag = 0x7FFF7FFFu;
-        uint32_t m = __vmaxu2(__vmaxu2(v.x & kMag, v.y & kMag), __vmaxu2(v.z & kMag, v.w & kMag));
-        m = __vmaxu2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-        m = __vmaxu2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-        m = max(m & 0xFFFFu, m >> 16);
-        if constexpr (DT == MQ_BF16) return m << 16;
-        return __float_as_uint(__half2float(__ushort_as_half((unsigned short)m))) & 0x7FFFFFFFu;
+__device__ __forceinline__ uint32_t max_abs(uint32_t a, uint32_t b) {
+    uint32_t r;
+    if constexpr (DT == MQ_BF16) asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    else if constexpr (DT == MQ_F16) asm("max.NaN.xorsign.abs.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    else asm("max.NaN.xorsign.abs.f32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// N consecutive elements of one lane as loaded: 16-byte words, or 32-byte ones
+// where the rows are aligned to that.
+template <int DT, int N>
+struct Raw {
+    static constexpr int kBytes = DT == MQ_F32 ? 4 : 2, kWords = N * kBytes / 4;
+    uint32_t w[kWords];
+    template <bool WIDE>
+    __device__ void load(const void *p) {
+        if constexpr (WIDE) {
+#pragma unroll
+            for (int i = 0; i < kWords; i += 8)
+                asm volatile("ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                             : "=r"(w[i]), "=r"(w[i + 1]), "=r"(w[i + 2]), "=r"(w[i + 3]), "=r"(w[i + 4]),
+                               "=r"(w[i + 5]), "=r"(w[i + 6]), "=r"(w[i + 7])
+                             : "l"(static_cast<const uint8_t *>(p) + 4 * i));
+        } else {
+#pragma unroll
+            for (int i = 0; i < kWords; i += 4) {
+                const uint4 v = *reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(p) + 4 * i);
+                w[i] = v.x; w[i + 1] = v.y; w[i + 2] = v.z; w[i + 3] = v.w;
+            }
+        }
     }
-    __device__ void get(float (&f)[8]) const {
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    __device__ void zero() {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) w[i] = 0u;
+    }
+    // Largest magnitude of the 32 / N adjacent lanes that hold a block, as fp32 bits.
+    __device__ uint32_t amax() const {
+        uint32_t m = w[0];
+#pragma unroll
+        for (int i = 1; i < kWords; ++i) m = max_abs<DT>(m, w[i]);
+#pragma unroll
+        for (int l = 1; l < 32 / N; l *= 2) m = max_abs<DT>(m, __shfl_xor_sync(0xFFFFFFFFu, m, l));
+        if constexpr (DT == MQ_F32) return m & 0x7FFFFFFFu;
+        m = max_abs<DT>(m, m >> 16) & 0x7FFFu;
+        if constexpr (DT == MQ_BF16) return m << 16;
+        return __float_as_uint(__half2float(__ushort_as_half((unsigned short)m)));
+    }
+    // Eight of the elements as fp32, from element 8 h.
+    __device__ void get(int h, float (&f)[8]) const {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            if constexpr (DT == MQ_BF16) {
-                f[2 * i] = __uint_as_float(w[i] << 16);
-                f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+            if constexpr (DT == MQ_F32) {
+                f[2 * i] = __uint_as_float(w[8 * h + 2 * i]);
+                f[2 * i + 1] = __uint_as_float(w[8 * h + 2 * i + 1]);
+            } else if constexpr (DT == MQ_BF16) {
+                f[2 * i] = __uint_as_float(w[4 * h + i] << 16);
+                f[2 * i + 1] = __uint_as_float(w[4 * h + i] & 0xFFFF0000u);
             } else {
-                const float2 t = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
+                const float2 t = __half22float2(*reinterpret_cast<const __half2 *>(&w[4 * h + i]));
                 f[2 * i] = t.x;
                 f[2 * i + 1] = t.y;
             }
         }
     }
 };
-template <>
-struct Raw8<MQ_F32> {
-    uint4 a, b;
-    static constexpr int kBytes = 4;
-    __device__ void load(const void *p) {
-        a = __ldcs(reinterpret_cast<const uint4 *>(p));
-        b = __ldcs(reinterpret_cast<const uint4 *>(p) + 1);
-    }
-    __device__ void zero() { a = b = make_uint4(0u, 0u, 0u, 0u); }
-    __device__ uint32_t amax() const {
-        const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-        uint32_t m = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) m = max(m, w[i] & 0x7FFFFFFFu);
-        m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-        return max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-    }
-    __device__ void get(float (&f)[8]) const {
-        const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(w[i]);
-    }
-};
 
-// Rows per warp and step: so many 16-byte loads of a thread are in flight.
-__host__ __device__ constexpr int quant_rows(int dtype) { return dtype == MQ_F32 ? 4 : 8; }
+// Rows per warp and step: so many loads of a thread are in flight.
+__host__ __device__ constexpr int quant_rows(int dtype) { return dtype == MQ_F32 ? 2 : 4; }
+constexpr int kQuantCols = 512;               // columns of a warp, 16 a lane
 constexpr int kDeqRows = 8;
 
-// One warp: 256 columns of a few rows (all in one 128-row band).  Steps beyond
+// One warp: 512 columns of a few rows (all in one 128-row band).  Steps beyond
 // the matrix (the padding rows and columns of the scale blocks) write zero scale
 // bytes only.
-template <int DT>
+template <int DT, bool WIDE>
 __global__ void __launch_bounds__(256)
-mx_quantize_kernel(const uint8_t *__restrict__ X, int64_t rows, int64_t K, int64_t ld_bytes,
-                   uint8_t *__restrict__ codes, uint8_t *__restrict__ scales) {
+mx_quantize_kernel(const uint8_t *__restrict__ X, int64_t rows, int64_t K, int64_t ld_bytes, uint32_t C,
+                   uint32_t total, uint8_t *__restrict__ codes, uint8_t *__restrict__ scales) {
     constexpr int kRows = quant_rows(DT);
     sm100::pdl_wait();
     sm100::pdl_launch_dependents();
     const int lane = threadIdx.x & 31;
-    const int64_t G = mx_groups(K), C = (K + 255) / 256, steps = (rows + 127) / 128 * (128 / kRows);
-    const int64_t total = steps * C, nwarps = ((int64_t)gridDim.x * blockDim.x) >> 5;
-    for (int64_t i = (blockIdx.x * (int64_t)blockDim.x + threadIdx.x) >> 5; i < total; i += nwarps) {
-        const int64_t r0 = i / C * kRows, c = (i % C) * 256 + lane * 8;
+    const int64_t G = mx_groups(K);
+    const uint32_t nwarps = gridDim.x * 8;
+    for (uint32_t i = blockIdx.x * 8 + (threadIdx.x >> 5); i < total; i += nwarps) {
+        const uint32_t q = i / C;
+        const int64_t r0 = (int64_t)q * kRows, c = (int64_t)(i - q * C) * kQuantCols + lane * 16;
         const int live = c < K ? (int)(rows - r0 < kRows ? (rows > r0 ? rows - r0 : 0) : kRows) : 0;
-        const uint8_t *src = X + r0 * ld_bytes + c * Raw8<DT>::kBytes;
-        Raw8<DT> raw[kRows];
+        const uint8_t *src = X + r0 * ld_bytes + c * Raw<DT, 16>::kBytes;
+        Raw<DT, 16> raw[kRows];
 #pragma unroll
         for (int j = 0; j < kRows; ++j) {
-            if (j < live) raw[j].load(src + j * ld_bytes);
+            if (j < live) raw[j].template load<WIDE>(src);
             else raw[j].zero();
+            src += ld_bytes;
         }
         uint8_t *dst = codes + r0 * (K / 2) + c / 2;
-        uint8_t *sc = scales + mx_scale_at(r0, c >> 7, G) + ((lane >> 2) & 3);   // 16 bytes a row
-        const bool write_scale = (lane & 3) == 0 && c < G * 128;
+        uint8_t *sc = scales + mx_scale_at(r0, c >> 7, G) + ((lane >> 1) & 3);   // 16 bytes a row
+        const bool write_scale = (lane & 1) == 0 && c < G * 128;
 #pragma unroll
         for (int j = 0; j < kRows; ++j) {
             const uint32_t E = mx_scale_byte(raw[j].amax());
             if (write_scale) sc[j * 16] = (uint8_t)E;
             if (j < live) {
-                float f[8];
-                raw[j].get(f);
-                *reinterpret_cast<uint32_t *>(dst + j * (K / 2)) = E == 255u ? 0u : scaled_codes8(f, mx_inverse(E));
+                uint2 code = make_uint2(0u, 0u);
+                if (E != 255u) {
+                    const float inv = mx_inverse(E);
+                    float f[8];
+                    raw[j].get(0, f);
+                    code.x = scaled_codes8(f, inv);
+                    raw[j].get(1, f);
+                    code.y = scaled_codes8(f, inv);
+                }
+                *reinterpret_cast<uint2 *>(dst) = code;
             }
+            dst += K / 2;
         }
     }
 }
@@ -145,21 +168,22 @@ mx_quantize_kernel(const uint8_t *__restrict__ X, int64_t rows, int64_t K, int64
 // columns of one row.
 template <int S>
 __global__ void __launch_bounds__(256)
-mx_slices_kernel(const uint8_t *__restrict__ X, int64_t M, int64_t K, int64_t ld_bytes, int tpt, int bn,
-                 int band_rows, uint8_t *__restrict__ codes, uint8_t *__restrict__ scales) {
+mx_slices_kernel(const uint8_t *__restrict__ X, int64_t K, int64_t ld_bytes, uint32_t C, uint32_t total,
+                 uint32_t tpt, int bn, int band_rows, uint8_t *__restrict__ codes, uint8_t *__restrict__ scales) {
     sm100::pdl_wait();                        // X may come from the previous kernel
     sm100::pdl_launch_dependents();
     const int lane = threadIdx.x & 31;
-    const int64_t G = mx_groups(K), C = (K + 255) / 256;
-    const int64_t total = M * C, nwarps = ((int64_t)gridDim.x * blockDim.x) >> 5;
-    for (int64_t i = (blockIdx.x * (int64_t)blockDim.x + threadIdx.x) >> 5; i < total; i += nwarps) {
-        const int64_t m = i / C, c = (i % C) * 256 + lane * 8, tile = m / tpt;
-        const int local = (int)(m - tile * tpt) * S;
-        Raw8<MQ_BF16> raw;
-        if (c < K) raw.load(X + m * ld_bytes + c * 2);
+    const int64_t G = mx_groups(K);
+    const uint32_t nwarps = gridDim.x * 8;
+    for (uint32_t i = blockIdx.x * 8 + (threadIdx.x >> 5); i < total; i += nwarps) {
+        const uint32_t q = i / C, tl = q / tpt;
+        const int64_t m = q, c = (int64_t)(i - q * C) * 256 + lane * 8, tile = tl;
+        const int local = (int)(q - tl * tpt) * S;
+        Raw<MQ_BF16, 8> raw;
+        if (c < K) raw.load<false>(X + m * ld_bytes + c * 2);
         else raw.zero();
         float u[8];
-        raw.get(u);
+        raw.get(0, u);
         uint32_t E = mx_slice0_byte(raw.amax());
         const bool bad = E == 255u;
         const float inv = bad ? 0.f : mx_inverse(E);
@@ -182,14 +206,15 @@ mx_slices_kernel(const uint8_t *__restrict__ X, int64_t M, int64_t K, int64_t ld
 template <bool F32>
 __global__ void __launch_bounds__(256)
 mx_dequantize_kernel(const uint8_t *__restrict__ codes, const uint8_t *__restrict__ scales, int64_t rows,
-                     int64_t K, uint8_t *__restrict__ out, int64_t ld_bytes) {
+                     int64_t K, uint32_t C, uint32_t total, uint8_t *__restrict__ out, int64_t ld_bytes) {
     sm100::pdl_wait();
     sm100::pdl_launch_dependents();
     const int lane = threadIdx.x & 31;
-    const int64_t G = mx_groups(K), C = (K + 255) / 256, steps = (rows + kDeqRows - 1) / kDeqRows;
-    const int64_t total = steps * C, nwarps = ((int64_t)gridDim.x * blockDim.x) >> 5;
-    for (int64_t i = (blockIdx.x * (int64_t)blockDim.x + threadIdx.x) >> 5; i < total; i += nwarps) {
-        const int64_t r0 = i / C * kDeqRows, c = (i % C) * 256 + lane * 8;
+    const int64_t G = mx_groups(K);
+    const uint32_t nwarps = gridDim.x * 8;
+    for (uint32_t i = blockIdx.x * 8 + (threadIdx.x >> 5); i < total; i += nwarps) {
+        const uint32_t q = i / C;
+        const int64_t r0 = (int64_t)q * kDeqRows, c = (int64_t)(i - q * C) * 256 + lane * 8;
         if (c >= K) continue;
         const int live = rows - r0 < kDeqRows ? (int)(rows - r0) : kDeqRows;
         const uint8_t *src = codes + r0 * (K / 2) + c / 2;
@@ -288,59 +313,70 @@ __device__ __forceinline__ uint32_t nested_block(const uint32_t (&P)[8], float s
     return E;
 }
 
-// One thread: one word of each plane, which is one block of MXFP4; four adjacent
-// lanes hold a row's 128 columns, so a warp reads 128 contiguous bytes of each
-// plane and writes whole 64-byte runs.  A block of threads takes whole 128 x 128
-// blocks, so nothing is divided per thread.
+// One thread: four words of each plane (rows 32 apart), each one block of MXFP4;
+// four adjacent lanes hold a row's 128 columns, so a warp reads 128 contiguous
+// bytes of each plane and writes whole 64-byte runs.  128 threads take one 128 x 128
+// block, so that what locates it is worked out once for 128 elements a thread.
 template <int R>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(128)
 mx_from_nested_kernel(const uint32_t *__restrict__ planes, const uint16_t *__restrict__ s16,
-                      const uint16_t *__restrict__ z16, int64_t N, int64_t K,
+                      const uint16_t *__restrict__ z16, int64_t N, int64_t K, uint32_t G, uint32_t blocks,
                       uint8_t *__restrict__ codes, uint8_t *__restrict__ scales) {
     sm100::pdl_wait();
     sm100::pdl_launch_dependents();
-    const int64_t G = K / kGroup, blocks = (N + 127) / 128 * G, plane_words = blocks * 512;
+    constexpr int kWords = 4;
+    const int64_t plane_words = (int64_t)blocks * 512;
     const int w = threadIdx.x & 3, n0 = (int)(threadIdx.x >> 2);     // word and first row of this thread
-    for (int64_t block = blockIdx.x; block < blocks; block += gridDim.x) {
-        const int64_t t = block / G, g = block - t * G;
-        uint32_t P[2][8];
-        float s[2], z[2];
+    for (uint32_t block = blockIdx.x; block < blocks; block += gridDim.x) {
+        const uint32_t t = block / G, g = block - t * G;
+        const uint32_t *src = planes + (int64_t)block * 512 + threadIdx.x;
+        uint32_t P[kWords][8];
+        float s[kWords], z[kWords];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < kWords; ++h) {
 #pragma unroll
-            for (int p = 0; p < 8; ++p)
-                P[h][p] = p < R ? __ldcs(planes + p * plane_words + block * 512 + h * 256 + threadIdx.x) : 0u;
-            s[h] = __half2float(__ushort_as_half(s16[block * 128 + h * 64 + n0]));
-            z[h] = z16 ? __half2float(__ushort_as_half(z16[block * 128 + h * 64 + n0])) : 128.f;
+            for (int p = 0; p < 8; ++p) P[h][p] = p < R ? __ldcs(src + p * plane_words + h * 128) : 0u;
+            s[h] = __half2float(__ushort_as_half(s16[(int64_t)block * 128 + h * 32 + n0]));
+            z[h] = z16 ? __half2float(__ushort_as_half(z16[(int64_t)block * 128 + h * 32 + n0])) : 128.f;
         }
+        const int64_t row = (int64_t)t * 128 + n0;
+        uint8_t *dst = codes + row * (K / 2) + g * 64 + w * 16, *sc = scales + mx_scale_at(row, g, G) + w;
+        const int left = N - row > 128 ? 128 : (int)(N - row);       // rows from this thread's first on
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int64_t row = t * 128 + h * 64 + n0;
+        for (int h = 0; h < kWords; ++h) {
             uint32_t c[4];
             const uint32_t E = nested_block<R>(P[h], s[h], z[h], c);
-            scales[mx_scale_at(row, g, G) + w] = (uint8_t)(row < N ? E : 0u);
-            if (row < N)
-                *reinterpret_cast<uint4 *>(codes + row * (K / 2) + g * 64 + w * 16) = make_uint4(c[0], c[1], c[2], c[3]);
+            sc[h * 4] = (uint8_t)(h * 32 < left ? E : 0u);           // rows 32 on: the next four bytes
+            if (h * 32 < left) *reinterpret_cast<uint4 *>(dst + h * 32 * (K / 2)) = make_uint4(c[0], c[1], c[2], c[3]);
         }
     }
 }
 
-int grid_for(int64_t work, int per_block) {
-    int64_t g = (work + per_block - 1) / per_block;
-    if (g > 148 * 32) g = 148 * 32;
-    return (int)(g < 1 ? 1 : g);
+// Warp-sized steps of a converter (some columns of some rows, 32-bit numbers: a
+// matrix of 2^43 elements is refused) and blocks of eight warps for them.
+struct Steps {
+    uint32_t C, total;
+    int grid;
+};
+bool steps_for(int64_t row_steps, int64_t K, int cols, Steps *s) {
+    const int64_t C = (K + cols - 1) / cols;
+    if (row_steps > (int64_t)UINT32_MAX / 2 / C) return false;
+    s->C = (uint32_t)C;
+    s->total = (uint32_t)(row_steps * C);
+    s->grid = (int)((s->total + 7) / 8 < 148 * 32 ? (s->total + 7) / 8 : 148 * 32);
+    return true;
 }
 
-// 256 threads a block, allowed to start before the previous kernel has ended
+// Blocks of `threads`, allowed to start before the previous kernel has ended
 // (every kernel here waits for it before it reads or writes anything).
 template <class... P, class... A>
-cudaError_t launch_pdl(void (*fn)(P...), int grid, cudaStream_t st, A... args) {
+cudaError_t launch_pdl(void (*fn)(P...), int grid, int threads, cudaStream_t st, A... args) {
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid);
-    cfg.blockDim = dim3(256);
+    cfg.blockDim = dim3((unsigned)threads);
     cfg.stream = st;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
@@ -366,9 +402,12 @@ mq_status check_mx4(const mq_mx4 *m, const char *what) {
 
 mq_status launch_mx_slices(const uint16_t *X, int64_t M, int64_t K, int64_t ldx, const MxSlicing &sl,
                            uint8_t *codes, uint8_t *scales, cudaStream_t st) {
+    Steps n;
+    if (!steps_for(M, K, 256, &n)) return fail(MQ_ERR_UNSUPPORTED, "mq_mx4_gemm_bf16: X is too large");
     const cudaError_t e =
-        launch_pdl(sl.S == 6 ? mx_slices_kernel<6> : mx_slices_kernel<8>, grid_for(M * ((K + 255) / 256) * 32, 256), st,
-                   reinterpret_cast<const uint8_t *>(X), M, K, ldx * 2, sl.tpt, sl.bn, sl.Tb ? 256 : 128, codes, scales);
+        launch_pdl(sl.S == 6 ? mx_slices_kernel<6> : mx_slices_kernel<8>, n.grid, 256, st,
+                   reinterpret_cast<const uint8_t *>(X), K, ldx * 2, n.C, n.total, sl.tpt, sl.bn, sl.Tb ? 256 : 128,
+                   codes, scales);
     return e == cudaSuccess ? MQ_OK : cuda_fail(e, "mx_slices_kernel");
 }
 
@@ -400,12 +439,17 @@ extern "C" mq_status mq_mx4_quantize(const void *X, int dtype, int64_t rows, int
     cudaStream_t st = (cudaStream_t)stream;
     const mq_status bs = bind_device(st);
     if (bs != MQ_OK) return bs;
-    const int grid = grid_for((rows + 127) / 128 * (128 / quant_rows(dtype)) * ((K + 255) / 256) * 32, 256);
+    Steps n;
+    if (!steps_for((rows + 127) / 128 * (128 / quant_rows(dtype)), K, kQuantCols, &n))
+        return fail(MQ_ERR_UNSUPPORTED, "mq_mx4_quantize: the matrix is too large");
     const uint8_t *x = static_cast<const uint8_t *>(X);
-    const auto fn = dtype == MQ_BF16  ? mx_quantize_kernel<MQ_BF16>
-                    : dtype == MQ_F16 ? mx_quantize_kernel<MQ_F16>
-                                      : mx_quantize_kernel<MQ_F32>;
-    const cudaError_t e = launch_pdl(fn, grid, st, x, rows, K, ld * size, codes_out, scales_out);
+    // 32-byte loads where every row starts on 32 bytes
+    const bool wide = (reinterpret_cast<uintptr_t>(X) | (uintptr_t)(rows > 1 ? ld * size : 0)) % 32 == 0;
+    const auto fn = dtype == MQ_BF16  ? wide ? mx_quantize_kernel<MQ_BF16, true> : mx_quantize_kernel<MQ_BF16, false>
+                    : dtype == MQ_F16 ? wide ? mx_quantize_kernel<MQ_F16, true> : mx_quantize_kernel<MQ_F16, false>
+                    : wide            ? mx_quantize_kernel<MQ_F32, true>
+                                      : mx_quantize_kernel<MQ_F32, false>;
+    const cudaError_t e = launch_pdl(fn, n.grid, 256, st, x, rows, K, ld * size, n.C, n.total, codes_out, scales_out);
     return e == cudaSuccess ? MQ_OK : cuda_fail(e, "mx_quantize_kernel");
 }
 
@@ -420,12 +464,16 @@ extern "C" mq_status mq_mx4_from_nested(const mq_weights *w, uint8_t *codes_out,
         return fail(MQ_ERR_MISALIGNED, "mq_mx4_from_nested: the outputs must be 16-byte aligned");
     cudaStream_t st = (cudaStream_t)stream;
     if ((s = bind_device(st)) != MQ_OK) return s;
-    using Fn = void (*)(const uint32_t *, const uint16_t *, const uint16_t *, int64_t, int64_t, uint8_t *, uint8_t *);
+    using Fn = void (*)(const uint32_t *, const uint16_t *, const uint16_t *, int64_t, int64_t, uint32_t, uint32_t,
+                        uint8_t *, uint8_t *);
     static const Fn fns[8] = {mx_from_nested_kernel<1>, mx_from_nested_kernel<2>, mx_from_nested_kernel<3>,
                               mx_from_nested_kernel<4>, mx_from_nested_kernel<5>, mx_from_nested_kernel<6>,
                               mx_from_nested_kernel<7>, mx_from_nested_kernel<8>};
-    const int grid = grid_for((w->N + 127) / 128 * (w->K / kGroup), 1);
-    const cudaError_t e = launch_pdl(fns[w->r - 1], grid, st, w->planes, w->scales, w->zeros, w->N, w->K, codes_out, scales_out);
+    const int64_t blocks = (w->N + 127) / 128 * (w->K / kGroup);
+    if (blocks > (int64_t)UINT32_MAX / 2) return fail(MQ_ERR_UNSUPPORTED, "mq_mx4_from_nested: the matrix is too large");
+    const int grid = (int)(blocks < 148 * 32 ? blocks : 148 * 32);
+    const cudaError_t e = launch_pdl(fns[w->r - 1], grid, 128, st, w->planes, w->scales, w->zeros, w->N, w->K,
+                                     w->K / kGroup, blocks, codes_out, scales_out);
     return e == cudaSuccess ? MQ_OK : cuda_fail(e, "mx_from_nested_kernel");
 }
 
@@ -442,9 +490,11 @@ extern "C" mq_status mq_mx4_dequantize(const mq_mx4 *m, void *out, int dtype, in
         return fail(MQ_ERR_MISALIGNED, "mq_mx4_dequantize: out and its row stride must be 16-byte aligned");
     cudaStream_t st = (cudaStream_t)stream;
     if ((s = bind_device(st)) != MQ_OK) return s;
-    const int grid = grid_for((m->rows + kDeqRows - 1) / kDeqRows * ((m->K + 255) / 256) * 32, 256);
+    Steps n;
+    if (!steps_for((m->rows + kDeqRows - 1) / kDeqRows, m->K, 256, &n))
+        return fail(MQ_ERR_UNSUPPORTED, "mq_mx4_dequantize: the matrix is too large");
     uint8_t *o = static_cast<uint8_t *>(out);
-    const cudaError_t e = launch_pdl(dtype == MQ_F32 ? mx_dequantize_kernel<true> : mx_dequantize_kernel<false>, grid, st,
-                                     m->codes, m->scales, m->rows, m->K, o, ld * size);
+    const cudaError_t e = launch_pdl(dtype == MQ_F32 ? mx_dequantize_kernel<true> : mx_dequantize_kernel<false>, n.grid,
+                                     256, st, m->codes, m->scales, m->rows, m->K, n.C, n.total, o, ld * size);
     return e == cudaSuccess ? MQ_OK : cuda_fail(e, "mx_dequantize_kernel");
 }
