@@ -110,7 +110,7 @@ struct Raw {
 // Rows per warp and step: so many loads of a thread are in flight.
 __host__ __device__ constexpr int quant_rows(int dtype) { return dtype == MQ_F32 ? 2 : 4; }
 constexpr int kQuantCols = 512;               // columns of a warp, 16 a lane
-constexpr int kDeqRows = 8;
+constexpr int kDeqRows = 4;
 
 // One warp: 512 columns of a few rows (all in one 128-row band).  Steps beyond
 // the matrix (the padding rows and columns of the scale blocks) write zero scale
@@ -202,8 +202,21 @@ mx_slices_kernel(const uint8_t *__restrict__ X, int64_t K, int64_t ld_bytes, uin
     }
 }
 
-// One warp: 256 columns of a few rows.
-template <bool F32>
+// 32 bytes of results: one store where rows are aligned to that, else two.
+template <bool WIDE>
+__device__ __forceinline__ void store32(void *p, const uint32_t (&v)[8]) {
+    if constexpr (WIDE) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]),
+                     "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                     : "memory");
+    } else {
+        static_cast<uint4 *>(p)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+        static_cast<uint4 *>(p)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+    }
+}
+
+// One warp: 512 columns of a few rows, 16 a lane.
+template <bool F32, bool WIDE>
 __global__ void __launch_bounds__(256)
 mx_dequantize_kernel(const uint8_t *__restrict__ codes, const uint8_t *__restrict__ scales, int64_t rows,
                      int64_t K, uint32_t C, uint32_t total, uint8_t *__restrict__ out, int64_t ld_bytes) {
@@ -214,43 +227,48 @@ mx_dequantize_kernel(const uint8_t *__restrict__ codes, const uint8_t *__restric
     const uint32_t nwarps = gridDim.x * 8;
     for (uint32_t i = blockIdx.x * 8 + (threadIdx.x >> 5); i < total; i += nwarps) {
         const uint32_t q = i / C;
-        const int64_t r0 = (int64_t)q * kDeqRows, c = (int64_t)(i - q * C) * 256 + lane * 8;
+        const int64_t r0 = (int64_t)q * kDeqRows, c = (int64_t)(i - q * C) * kQuantCols + lane * 16;
         if (c >= K) continue;
         const int live = rows - r0 < kDeqRows ? (int)(rows - r0) : kDeqRows;
         const uint8_t *src = codes + r0 * (K / 2) + c / 2;
         const uint8_t *sc = scales + mx_scale_at(r0, c >> 7, G) + ((c >> 5) & 3);
         uint8_t *dst = out + r0 * ld_bytes + c * (F32 ? 4 : 2);
-        uint32_t w[kDeqRows], E[kDeqRows];
+        uint2 w[kDeqRows];
+        uint32_t E[kDeqRows];
 #pragma unroll
         for (int j = 0; j < kDeqRows; ++j) {
-            w[j] = E[j] = 0;
+            w[j] = make_uint2(0u, 0u);
+            E[j] = 0;
             if (j < live) {
-                w[j] = __ldcs(reinterpret_cast<const uint32_t *>(src + j * (K / 2)));
+                w[j] = *reinterpret_cast<const uint2 *>(src);
                 E[j] = sc[j * 16];
             }
+            src += K / 2;
         }
 #pragma unroll
         for (int j = 0; j < kDeqRows; ++j) {
             if (j >= live) break;
-            float u[8];
-            mx_units8(w[j], u);
             const uint64_t s2 = pair(mx_value(E[j]), mx_value(E[j]));
+            uint32_t v[16];                                         // fp32 bits, or bf16 pairs in the first eight
 #pragma unroll
-            for (int e = 0; e < 4; ++e)                             // exact (at most 2 significant bits)
-                unpair(mul2(pair(u[2 * e], u[2 * e + 1]), s2), u[2 * e], u[2 * e + 1]);
-            if constexpr (F32) {
-                float4 *q = reinterpret_cast<float4 *>(dst + j * ld_bytes);
-                q[0] = make_float4(u[0], u[1], u[2], u[3]);
-                q[1] = make_float4(u[4], u[5], u[6], u[7]);
-            } else {
-                uint32_t h[4];
+            for (int h = 0; h < 2; ++h) {
+                float u[8];
+                mx_units8(h ? w[j].y : w[j].x, u);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const __nv_bfloat162 b = __floats2bfloat162_rn(u[2 * e], u[2 * e + 1]);
-                    h[e] = *reinterpret_cast<const uint32_t *>(&b);
+                for (int e = 0; e < 4; ++e) {                       // exact (at most 2 significant bits)
+                    unpair(mul2(pair(u[2 * e], u[2 * e + 1]), s2), u[2 * e], u[2 * e + 1]);
+                    if constexpr (F32) {
+                        v[8 * h + 2 * e] = __float_as_uint(u[2 * e]);
+                        v[8 * h + 2 * e + 1] = __float_as_uint(u[2 * e + 1]);
+                    } else {
+                        const __nv_bfloat162 b = __floats2bfloat162_rn(u[2 * e], u[2 * e + 1]);
+                        v[4 * h + e] = *reinterpret_cast<const uint32_t *>(&b);
+                    }
                 }
-                *reinterpret_cast<uint4 *>(dst + j * ld_bytes) = make_uint4(h[0], h[1], h[2], h[3]);
             }
+            store32<WIDE>(dst, {v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7]});
+            if constexpr (F32) store32<WIDE>(dst + 32, {v[8], v[9], v[10], v[11], v[12], v[13], v[14], v[15]});
+            dst += ld_bytes;
         }
     }
 }
@@ -491,10 +509,13 @@ extern "C" mq_status mq_mx4_dequantize(const mq_mx4 *m, void *out, int dtype, in
     cudaStream_t st = (cudaStream_t)stream;
     if ((s = bind_device(st)) != MQ_OK) return s;
     Steps n;
-    if (!steps_for((m->rows + kDeqRows - 1) / kDeqRows, m->K, 256, &n))
+    if (!steps_for((m->rows + kDeqRows - 1) / kDeqRows, m->K, kQuantCols, &n))
         return fail(MQ_ERR_UNSUPPORTED, "mq_mx4_dequantize: the matrix is too large");
     uint8_t *o = static_cast<uint8_t *>(out);
-    const cudaError_t e = launch_pdl(dtype == MQ_F32 ? mx_dequantize_kernel<true> : mx_dequantize_kernel<false>, n.grid,
-                                     256, st, m->codes, m->scales, m->rows, m->K, n.C, n.total, o, ld * size);
+    const bool wide = (reinterpret_cast<uintptr_t>(out) | (uintptr_t)(m->rows > 1 ? ld * size : 0)) % 32 == 0;
+    const auto fn = dtype == MQ_F32 ? wide ? mx_dequantize_kernel<true, true> : mx_dequantize_kernel<true, false>
+                    : wide          ? mx_dequantize_kernel<false, true>
+                                    : mx_dequantize_kernel<false, false>;
+    const cudaError_t e = launch_pdl(fn, n.grid, 256, st, m->codes, m->scales, m->rows, m->K, n.C, n.total, o, ld * size);
     return e == cudaSuccess ? MQ_OK : cuda_fail(e, "mx_dequantize_kernel");
 }
