@@ -282,50 +282,67 @@ __device__ __forceinline__ float scaled_level_odd(double s, double u, double z) 
     return (double)f == w ? f : __uint_as_float(__float_as_uint(f) | 1u);
 }
 
+// Zero points outside 32 <= z < 4096 (none in practice), out of line: the levels
+// in 64 bits, cut with a sticky bit.  Returns the scale byte, codes in c.
+template <int R>
+__device__ __noinline__ uint32_t nested_block_any(const uint32_t *B, float s, float z, uint32_t *c) {
+    constexpr double kHalf = R == 8 ? 0.5 : (double)(1 << (7 - R > 0 ? 7 - R : 0));
+    uint32_t m = 0;
+    for (int j = 0; j < 32; ++j) {
+        const float v = scaled_level_odd(s, (double)((B[j & 7] >> (8 * (j >> 3))) & 0xFFu) + kHalf, z);
+        m = max(m, __float_as_uint(v) & 0x7FFFFFFFu);
+    }
+    const uint32_t E = mx_scale_byte(m);
+    const float f = E == 255u ? 0.f : mx_inverse(E);
+#pragma unroll 1
+    for (int b = 0; b < 4; ++b) {
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            v[e] = scaled_level_odd(s, (double)((B[e] >> (8 * b)) & 0xFFu) + kHalf, z);
+        c[b] = E == 255u ? 0u : scaled_codes8(v, f);
+    }
+    return E;
+}
+
 // The block (32 columns of a row, one word of each plane) as MXFP4: returns the
 // scale byte, codes in c.
-template <int R>
+template <int R, bool ASYM>
 __device__ __forceinline__ uint32_t nested_block(const uint32_t (&P)[8], float s, float z, uint32_t (&c)[4]) {
     constexpr float kHalf = R == 8 ? 0.5f : (float)(1 << (7 - R > 0 ? 7 - R : 0));   // 2^(7-r)
     uint32_t B[8];
     byte_words<R>(P, B);                                             // byte b of B[e]: column 8 b + e
-    float v[4][8];
-    uint32_t E;
-    float f;
-    if (z >= 32.f && z < 4096.f) {
-        // The level minus z has at most 13 significant bits here, so its product
-        // with the 11 bits of s is exact in fp32, and so is every step: a byte
-        // is set into 2^15 + byte by one permute, the rest is one addition and,
-        // once the block's largest level is known, one multiplication by s
-        // times the power of two.
-        const uint64_t off = pair(kHalf - z - 32768.f, kHalf - z - 32768.f);
-        float m = 0.f;
+    if constexpr (ASYM) {
+        if (!(z >= 32.f && z < 4096.f)) {
+            uint32_t Bm[8], cm[4];
 #pragma unroll
-        for (int b = 0; b < 4; ++b)
+            for (int e = 0; e < 8; ++e) Bm[e] = B[e];
+            const uint32_t E = nested_block_any<R>(Bm, s, z, cm);
 #pragma unroll
-            for (int e = 0; e < 8; e += 2) {
-                const uint32_t sel = 0x7604u | ((uint32_t)b << 4);
-                const uint64_t t = add2(pair(__uint_as_float(prmt(B[e], 0x47000000u, sel)),
-                                             __uint_as_float(prmt(B[e + 1], 0x47000000u, sel))), off);
-                unpair(t, v[b][e], v[b][e + 1]);
-                m = fmaxf(m, fmaxf(fabsf(v[b][e]), fabsf(v[b][e + 1])));
-            }
-        const float a = s * m;
-        E = mx_scale_byte(__float_as_uint(a));
-        f = a > 0.f ? s * mx_inverse(E) : s;                         // all zeros: keep their signs
-    } else {
-        // other zero points (none in practice): 64 bits, cut with a sticky bit
-        uint32_t m = 0;
-#pragma unroll
-        for (int b = 0; b < 4; ++b)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                v[b][e] = scaled_level_odd(s, (double)((B[e] >> (8 * b)) & 0xFFu) + (double)kHalf, z);
-                m = max(m, __float_as_uint(v[b][e]) & 0x7FFFFFFFu);
-            }
-        E = mx_scale_byte(m);
-        f = E == 255u ? 0.f : mx_inverse(E);
+            for (int b = 0; b < 4; ++b) c[b] = cm[b];
+            return E;
+        }
     }
+    // The level minus z has at most 13 significant bits here, so its product
+    // with the 11 bits of s is exact in fp32, and so is every step: a byte is
+    // set into 2^15 + byte by one permute, the rest is one addition and, once
+    // the block's largest level is known, one multiplication by s times the
+    // power of two.
+    float v[4][8], m = 0.f;
+    const uint64_t off = pair(kHalf - z - 32768.f, kHalf - z - 32768.f);
+#pragma unroll
+    for (int b = 0; b < 4; ++b)
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) {
+            const uint32_t sel = 0x7604u | ((uint32_t)b << 4);
+            const uint64_t t = add2(pair(__uint_as_float(prmt(B[e], 0x47000000u, sel)),
+                                         __uint_as_float(prmt(B[e + 1], 0x47000000u, sel))), off);
+            unpair(t, v[b][e], v[b][e + 1]);
+            m = fmaxf(m, fmaxf(fabsf(v[b][e]), fabsf(v[b][e + 1])));
+        }
+    const float a = s * m;
+    const uint32_t E = mx_scale_byte(__float_as_uint(a));
+    const float f = a > 0.f ? s * mx_inverse(E) : s;                 // all zeros: keep their signs
 #pragma unroll
     for (int b = 0; b < 4; ++b) c[b] = E == 255u ? 0u : scaled_codes8(v[b], f);
     return E;
@@ -335,8 +352,8 @@ __device__ __forceinline__ uint32_t nested_block(const uint32_t (&P)[8], float s
 // four adjacent lanes hold a row's 128 columns, so a warp reads 128 contiguous
 // bytes of each plane and writes whole 64-byte runs.  128 threads take one 128 x 128
 // block, so that what locates it is worked out once for 128 elements a thread.
-template <int R>
-__global__ void __launch_bounds__(128)
+template <int R, bool ASYM>
+__global__ void __launch_bounds__(128, R <= 4 ? 7 : 5)
 mx_from_nested_kernel(const uint32_t *__restrict__ planes, const uint16_t *__restrict__ s16,
                       const uint16_t *__restrict__ z16, int64_t N, int64_t K, uint32_t G, uint32_t blocks,
                       uint8_t *__restrict__ codes, uint8_t *__restrict__ scales) {
@@ -355,7 +372,7 @@ mx_from_nested_kernel(const uint32_t *__restrict__ planes, const uint16_t *__res
 #pragma unroll
             for (int p = 0; p < 8; ++p) P[h][p] = p < R ? __ldcs(src + p * plane_words + h * 128) : 0u;
             s[h] = __half2float(__ushort_as_half(s16[(int64_t)block * 128 + h * 32 + n0]));
-            z[h] = z16 ? __half2float(__ushort_as_half(z16[(int64_t)block * 128 + h * 32 + n0])) : 128.f;
+            z[h] = ASYM ? __half2float(__ushort_as_half(z16[(int64_t)block * 128 + h * 32 + n0])) : 128.f;
         }
         const int64_t row = (int64_t)t * 128 + n0;
         uint8_t *dst = codes + row * (K / 2) + g * 64 + w * 16, *sc = scales + mx_scale_at(row, g, G) + w;
@@ -363,7 +380,7 @@ mx_from_nested_kernel(const uint32_t *__restrict__ planes, const uint16_t *__res
 #pragma unroll
         for (int h = 0; h < kWords; ++h) {
             uint32_t c[4];
-            const uint32_t E = nested_block<R>(P[h], s[h], z[h], c);
+            const uint32_t E = nested_block<R, ASYM>(P[h], s[h], z[h], c);
             sc[h * 4] = (uint8_t)(h * 32 < left ? E : 0u);           // rows 32 on: the next four bytes
             if (h * 32 < left) *reinterpret_cast<uint4 *>(dst + h * 32 * (K / 2)) = make_uint4(c[0], c[1], c[2], c[3]);
         }
@@ -484,13 +501,17 @@ extern "C" mq_status mq_mx4_from_nested(const mq_weights *w, uint8_t *codes_out,
     if ((s = bind_device(st)) != MQ_OK) return s;
     using Fn = void (*)(const uint32_t *, const uint16_t *, const uint16_t *, int64_t, int64_t, uint32_t, uint32_t,
                         uint8_t *, uint8_t *);
-    static const Fn fns[8] = {mx_from_nested_kernel<1>, mx_from_nested_kernel<2>, mx_from_nested_kernel<3>,
-                              mx_from_nested_kernel<4>, mx_from_nested_kernel<5>, mx_from_nested_kernel<6>,
-                              mx_from_nested_kernel<7>, mx_from_nested_kernel<8>};
+    static const Fn fns[2][8] = {
+        {mx_from_nested_kernel<1, false>, mx_from_nested_kernel<2, false>, mx_from_nested_kernel<3, false>,
+         mx_from_nested_kernel<4, false>, mx_from_nested_kernel<5, false>, mx_from_nested_kernel<6, false>,
+         mx_from_nested_kernel<7, false>, mx_from_nested_kernel<8, false>},
+        {mx_from_nested_kernel<1, true>, mx_from_nested_kernel<2, true>, mx_from_nested_kernel<3, true>,
+         mx_from_nested_kernel<4, true>, mx_from_nested_kernel<5, true>, mx_from_nested_kernel<6, true>,
+         mx_from_nested_kernel<7, true>, mx_from_nested_kernel<8, true>}};
     const int64_t blocks = (w->N + 127) / 128 * (w->K / kGroup);
     if (blocks > (int64_t)UINT32_MAX / 2) return fail(MQ_ERR_UNSUPPORTED, "mq_mx4_from_nested: the matrix is too large");
     const int grid = (int)(blocks < 148 * 32 ? blocks : 148 * 32);
-    const cudaError_t e = launch_pdl(fns[w->r - 1], grid, 128, st, w->planes, w->scales, w->zeros, w->N, w->K,
+    const cudaError_t e = launch_pdl(fns[w->zeros != nullptr][w->r - 1], grid, 128, st, w->planes, w->scales, w->zeros, w->N, w->K,
                                      w->K / kGroup, blocks, codes_out, scales_out);
     return e == cudaSuccess ? MQ_OK : cuda_fail(e, "mx_from_nested_kernel");
 }
