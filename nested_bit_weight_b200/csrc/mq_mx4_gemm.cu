@@ -83,8 +83,7 @@ struct MxCfg {
     // its parity cannot express.
     static_assert(kStages >= 4, "ring");
     static constexpr size_t kSmem = 1024 + (size_t)kStages * kStage + kParts + 1024;
-    // no more CTAs on an SM than tensor memory has room for: one that waited for
-    // columns could hold up the cluster that holds them
+    // no more CTAs on an SM than tensor memory has room for
     static_assert((512 / kCols + 1) * kSmem > 228 * 1024, "CTAs an SM");
 };
 
@@ -163,6 +162,15 @@ __device__ __forceinline__ void read_columns(uint32_t base, int slices, int live
     }
 }
 
+// The epilogue warps have read tensor memory: the MMA warp may give it back.  It
+// does so before any CTA waits for another's parts: a CTA that held columns
+// while it waited for one that still wants them could lock up with another
+// kernel's cluster that does the same the other way round.
+__device__ __forceinline__ void tmem_read() {
+    tc_fence_before();
+    named_arrive(2, 160);
+}
+
 // Epilogue of one thread: its row of the tile, straight to Y or in parts to the
 // CTAs that own the columns, which then add what they were sent.
 template <int BN, class T>
@@ -173,6 +181,7 @@ __device__ __forceinline__ void epilogue(const MxArgs &a, uint32_t base, float *
             read_columns<BN>(base, a.slices, a.M, [&](int col, const float (&y)[4]) {
                 if (n < a.N) store4<T>(a, col, n, y);
             });
+        tmem_read();
         return;
     }
     const int lper = a.lper, first = rank << lper, left = a.M - first, per = 1 << lper;
@@ -185,6 +194,7 @@ __device__ __forceinline__ void epilogue(const MxArgs &a, uint32_t base, float *
             st_async_v4(cluster_map(at, owner), y[0], y[1], y[2], y[3], cluster_map(bar0, owner));
         });
     }
+    tmem_read();
     if (groups <= 0) return;
     // never cut short, also when this CTA gave up: until then stores to this
     // CTA's memory may be on their way
@@ -392,22 +402,20 @@ mx4_gemm_kernel(const __grid_constant__ MxArgs a) {
         if (a.out == MQ_BF16) epilogue<BN, __nv_bfloat16>(a, base, parts, sent, rank, n, row, ok, flags);
         else if (a.out == MQ_F16) epilogue<BN, __half>(a, base, parts, sent, rank, n, row, ok, flags);
         else epilogue<BN, float>(a, base, parts, sent, rank, n, row, ok, flags);
-        tc_fence_before();
+    } else if (warp == 1) {
+        named_sync(2, 160);
+        tc_fence_after();
+        tmem_dealloc(*reinterpret_cast<volatile uint32_t *>(tmem_slot), C::kCols);
     }
 
-    // ---- end: copies and MMAs in flight land (already so unless a wait gave up)
+    // ---- end: copies in flight land (already so unless a wait gave up)
     __syncthreads();
     if (threadIdx.x == 0 && flags[0]) {
         atomicOr(&g_mx_timeout, 1u);
         for (int s = 0; s < kS && s < flags[1]; ++s)
             mbar_wait_bounded(full + s, (uint32_t)((flags[1] - 1 - s) / kS) & 1u);
     }
-    tc_fence_before();
-    __syncthreads();
-    if (warp == 1) {
-        tc_fence_after();
-        tmem_dealloc(*reinterpret_cast<volatile uint32_t *>(tmem_slot), C::kCols);
-    }
+    __syncthreads();                                          // shared memory stays until then
 }
 
 using MxFn = void (*)(MxArgs);

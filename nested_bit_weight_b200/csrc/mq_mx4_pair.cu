@@ -454,9 +454,9 @@ mq_status launch_mx_pair(const MxProduct &p, cudaStream_t st) {
     cudaError_t e;
     int64_t Ta, Tb;
     bool maps;
-    // TMA stores want row strides in 16 bytes, and cut a box off at the tensor's
-    // edge in steps of 16 bytes only
-    if (p.slices == 1 && p.ldy * size % 16 == 0 && w->rows * size % 16 == 0) {
+    // TMA stores want row strides in 16 bytes (below 2^40), and cut a box off at
+    // the tensor's edge in steps of 16 bytes only
+    if (p.slices == 1 && p.ldy * size % 16 == 0 && w->rows * size % 16 == 0 && p.ldy < ((int64_t)1 << 36)) {
         Ta = (p.M + 255) / 256;
         a.bn = 256;
         for (int bn : {192, 128})

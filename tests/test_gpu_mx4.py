@@ -213,7 +213,8 @@ def _rest(X, W, out="fp32"):
 SHAPES = [(1, 1, 32), (1, 128, 64), (1, 1024, 4096), (2, 130, 96), (3, 300, 4128), (5, 4096, 2048), (8, 129, 1056),
           (16, 256, 14336), (17, 1000, 288), (33, 640, 512), (64, 128, 256), (65, 200, 544), (128, 384, 1024),
           (129, 128, 4096), (255, 257, 800), (300, 1280, 2080), (1000, 700, 160), (25, 260, 288), (31, 264, 96),
-          (130, 5000, 512), (200, 5001, 512), (500, 640, 1312), (385, 321, 64)]
+          (130, 5000, 512), (200, 5001, 512), (500, 640, 1312), (385, 321, 64), (300, 1, 64), (300, 300, 32),
+          (2, 4096, 4096), (2, 5, 32), (24, 7, 32), (129, 8, 4096), (12, 20000, 160)]
 
 
 @pytest.mark.parametrize("out", ["bf16", "fp16", "fp32"])
@@ -408,6 +409,71 @@ def test_captured_graphs_replayed_with_new_inputs_and_side_by_side(M):
             X4 = mq.mx4_quantize(new[i])
             want = (mq.mx4_dequantize(X4), mq.mx4_gemm(X4, w4), mq.mx4_gemm_bf16(new[i], w4))
             assert all(torch.equal(a, b) for a, b in zip(outs[i], want))
+
+
+def test_first_calls_of_a_process_inside_a_capture():
+    # nothing is set up lazily that a capture does not allow
+    import os
+    import subprocess
+    import sys
+    code = """
+import torch
+import nested_bit_weight_b200 as mq
+torch.manual_seed(1)
+x, xb = (torch.randn(m, 512, device='cuda').bfloat16() for m in (1, 300))
+w = torch.randn(384, 512, device='cuda').bfloat16()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    w4 = mq.mx4_quantize(w)
+    out = [mq.mx4_gemm_bf16(x, w4), mq.mx4_gemm(mq.mx4_quantize(x), w4), mq.mx4_gemm_bf16(xb, w4),
+           mq.mx4_gemm(mq.mx4_quantize(xb), w4), mq.mx4_dequantize(w4)]
+g.replay()
+torch.cuda.synchronize()
+w4 = mq.mx4_quantize(w)
+want = [mq.mx4_gemm_bf16(x, w4), mq.mx4_gemm(mq.mx4_quantize(x), w4), mq.mx4_gemm_bf16(xb, w4),
+        mq.mx4_gemm(mq.mx4_quantize(xb), w4), mq.mx4_dequantize(w4)]
+assert all(torch.equal(a, b) for a, b in zip(out, want))
+mq.mq_device_status()
+print('captured first')
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert "captured first" in r.stdout, r.stdout + r.stderr
+
+
+def test_beside_and_between_the_nested_products():
+    # one stream: nested and MXFP4 products in turn, each launched while the one
+    # before still runs; two streams: both at once
+    import torch
+    mq = _mq()
+    N, K = 1024, 4096
+    codes, s, p = _nested(N, K, 3)
+    w4 = mq.mx4_from_nested(p, 4)
+    xs = {M: _acts(M, K, M) for M in (1, 16, 200)}
+    want = {}
+    for M, x in xs.items():
+        want[M] = [mq.gemm(x, p, 2), mq.mx4_gemm_bf16(x, w4), mq.gemm(x, p, 4), mq.mx4_gemm(mq.mx4_quantize(x), w4)]
+        torch.cuda.synchronize()
+    got = []
+    for _ in range(10):
+        for M, x in xs.items():
+            got.append((M, [mq.gemm(x, p, 2), mq.mx4_gemm_bf16(x, w4), mq.gemm(x, p, 4),
+                            mq.mx4_gemm(mq.mx4_quantize(x), w4)]))
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    pair = []
+    for _ in range(10):
+        for M, x in xs.items():
+            with torch.cuda.stream(a):
+                y = mq.gemm(x, p, 2)
+            with torch.cuda.stream(b):
+                pair.append((M, y, mq.mx4_gemm_bf16(x, w4), mq.mx4_gemm(mq.mx4_quantize(x), w4)))
+    torch.cuda.synchronize()
+    mq.mq_device_status()
+    for M, ys in got:
+        assert all(torch.equal(u, v) for u, v in zip(ys, want[M]))
+    for M, y, y16, y4 in pair:
+        assert torch.equal(y, want[M][0]) and torch.equal(y16, want[M][1]) and torch.equal(y4, want[M][3])
 
 
 def test_weights_quantized_right_before_the_product():
