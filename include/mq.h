@@ -390,6 +390,15 @@ MQ_API mq_status mq_gemv_noalloc(const uint16_t *X_dev, const mq_weights *w, int
  *           is at (i % 32) * 16 + (i / 32) * 4 + j.  Bytes of rows and
  *           columns beyond the matrix are 0.
  * Both buffers 16-byte aligned.
+ *
+ * Stream order.  The kernels below are launched with programmatic dependent
+ * launch, but read and write nothing before the preceding kernel of the stream
+ * has completed (the products only bring weights into L2 before that): any
+ * operand, the weights too, may be what the call before wrote.  They use no
+ * memory but their arguments, so calls on different streams need no ordering
+ * beyond that of the data.  They may be captured into CUDA graphs, also as the
+ * first calls of a process.  Waits inside the products are bounded as those of
+ * mq_gemm (mq_device_status).
  */
 typedef struct mq_mx4 {
     const uint8_t *codes;    /* device: mq_mx4_code_bytes(rows, K) bytes */
@@ -405,8 +414,10 @@ enum {
     MQ_F32 = 2
 };
 
-/* Bytes of the two buffers (0 on invalid sizes: rows < 0 or > 2^31 - 256, K
- * not a positive multiple of 32 or > 2^31 - 256; 0 also for rows = 0). */
+/*
+ * Bytes of the two buffers (0 on invalid sizes: rows < 0 or > 2^31 - 256, K not
+ * a positive multiple of 32 or > 2^31 - 256; 0 also for rows = 0).
+ */
 MQ_API size_t mq_mx4_code_bytes(int64_t rows, int64_t K);
 MQ_API size_t mq_mx4_scale_bytes(int64_t rows, int64_t K);
 
@@ -415,9 +426,10 @@ MQ_API size_t mq_mx4_scale_bytes(int64_t rows, int64_t K);
  *   X_dev       rows x K values of type dtype (MQ_BF16, MQ_F16, MQ_F32), row i
  *               at element i * ld
  *   codes_out, scales_out  the two buffers (all of their bytes are written)
- * Preconditions: the sizes above, ld >= K, X and the bytes of a row's stride
- * multiples of 16, the outputs 16-byte aligned and not overlapping X.
- * rows == 0 does nothing.
+ * Preconditions: the sizes above, ld >= K, X and (for more than one row) the
+ * bytes of a row's stride multiples of 16, the outputs 16-byte aligned and not
+ * overlapping X.  rows == 0 does nothing.  MQ_ERR_UNSUPPORTED from about 2^43
+ * elements on (also mq_mx4_from_nested, mq_mx4_dequantize).
  */
 MQ_API mq_status mq_mx4_quantize(const void *X_dev, int dtype, int64_t rows, int64_t K, int64_t ld,
                                  uint8_t *codes_out, uint8_t *scales_out, void *stream);
@@ -453,14 +465,17 @@ MQ_API mq_status mq_mx4_gemm(const mq_mx4 *X, const mq_mx4 *w, void *Y_dev, int 
 /*
  * Y = X . W^T with bf16 activations kept (weights only in 4 bits): single
  * tokens and small batches.  X is M x w->K bf16, row i at element i * ldx.  A
- * row of X is written as a sum of eight MXFP4 rows (within 2^-22 of the largest
- * value of each block of 32), which meet the weights on the 4-bit tensor
- * cores.
+ * row of X is written as a sum of MXFP4 rows ("slices"), which meet the weights
+ * on the 4-bit tensor cores: eight slices, which leave less than 2^-22 of the
+ * largest value of each block of 32; six for more than 16 rows with a 16-bit
+ * y_dtype, which leave less than 2^-16 (half a step of bf16 is 2^-9, of fp16
+ * 2^-12).  Blocks whose largest value is below 2^-100 lose what lies below
+ * 2^-129.
  *   workspace  device buffer of mq_mx4_gemm_bf16_workspace_bytes(M, N, K)
- *              bytes, contents arbitrary before and after (may be NULL when
- *              that is 0).  Calls that can overlap must not share it.
- * Preconditions as mq_mx4_gemm, and ldx >= K with a row's stride a multiple of
- * 16 bytes.
+ *              bytes (0 for M <= 2, when it may be NULL), contents arbitrary
+ *              before and after.  Calls that can overlap must not share it.
+ * Preconditions as mq_mx4_gemm, M <= 2^27, ldx >= K, and for more than one row
+ * a row's stride a multiple of 16 bytes.
  */
 MQ_API size_t mq_mx4_gemm_bf16_workspace_bytes(int64_t M, int64_t N, int64_t K);
 MQ_API mq_status mq_mx4_gemm_bf16(const uint16_t *X_dev, int64_t M, int64_t ldx, const mq_mx4 *w,
