@@ -404,16 +404,16 @@ def mq_mx4_gemm_bf16_workspace_bytes(M: int, N: int, K: int) -> int:
 # Small calls are bound by the host, so the common case of each function below
 # (tensors on the current device, its current stream) takes no detours: torch's
 # names are looked up once, and no context is entered.
-_torch = _empty = _u8 = _raw_stream = _get_device = None
+_torch = _u8 = _raw_stream = _get_device = None
 _types: dict = {}          # torch dtype -> MQ_* code
 
 
 def _init() -> None:
-    global _torch, _empty, _u8, _raw_stream, _get_device
+    global _torch, _u8, _raw_stream, _get_device
     import torch
     _types.update({torch.bfloat16: BF16, torch.float16: F16, torch.float32: F32})
     _raw_stream, _get_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
-    _torch, _empty, _u8 = torch, torch.empty, torch.uint8
+    _torch, _u8 = torch, torch.uint8
 
 
 def _dtype_code(dtype) -> int:
@@ -476,20 +476,11 @@ class _On:
         return self._ctx.__exit__(*exc)
 
 
-def _call(fn, device, stream, *args):
-    """fn(*args, stream handle) with the device and stream of the call current."""
-    i = device.index
-    if stream is None and i == _get_device():
-        return fn(*args, _raw_stream(i))
-    with _On(device, stream) as st:
-        return fn(*args, st)
-
-
 class Mx4Matrix:
     """A rows x K matrix in MXFP4 (device tensors): codes uint8 [rows, K/2] and
     the scale blocks (mq_mx4 in include/mq.h)."""
 
-    __slots__ = ("rows", "K", "device", "_ptrs", "_struct", "_codes", "_scales", "_buf")
+    _codes = _scales = _struct = None          # made when asked for
 
     def __init__(self, codes, scales, rows: int, K: int):
         if _torch is None:
@@ -501,7 +492,7 @@ class Mx4Matrix:
         if codes.device != scales.device:
             raise ValueError("codes and scales are on different devices")
         self.rows, self.K, self.device = rows, K, codes.device
-        self._codes, self._scales, self._buf, self._struct = codes, scales, None, None
+        self._codes, self._scales, self._like = codes, scales, codes
         self._ptrs = codes.data_ptr(), scales.data_ptr()
 
     @classmethod
@@ -509,36 +500,18 @@ class Mx4Matrix:
         """Uninitialised buffers for a rows x K matrix."""
         if _torch is None:
             _init()
-        return cls._new(rows, K, lambda n, dtype: _empty(n, dtype=dtype, device=device))
-
-    @classmethod
-    def _new(cls, rows: int, K: int, empty):
-        if rows < 0 or K < 32 or K % 32:
-            raise ValueError("need rows >= 0 and K a positive multiple of 32")
-        self = cls.__new__(cls)
-        # one allocation: the codes (rows of 16-byte multiples), then the scale blocks
-        nc = rows * (K >> 1)
-        self._buf = buf = empty(nc + ((rows + 127) >> 7) * ((K + 127) >> 7) * 512, dtype=_u8)
-        ptr = buf.data_ptr()
-        self._ptrs = ptr, ptr + nc
-        self.rows, self.K, self.device = rows, K, buf.device
-        self._codes = self._scales = self._struct = None
-        return self
-
-    @property
-    def _like(self):
-        return self._codes if self._buf is None else self._buf
+        return _new_mx4(rows, K, _torch.empty(0, device=device))
 
     @property
     def codes(self):
         if self._codes is None:
-            self._codes = self._buf[:self.rows * (self.K // 2)].view(self.rows, self.K // 2)
+            self._codes = self._like[:self.rows * (self.K // 2)].view(self.rows, self.K // 2)
         return self._codes
 
     @property
     def scales(self):
         if self._scales is None:
-            self._scales = self._buf[self.rows * (self.K // 2):]
+            self._scales = self._like[self.rows * (self.K // 2):]
         return self._scales
 
     @property
@@ -549,11 +522,25 @@ class Mx4Matrix:
         return s
 
 
+def _new_mx4(rows: int, K: int, like) -> Mx4Matrix:
+    """Uninitialised buffers on the device of the tensor `like`, in one allocation:
+    the codes (rows of 16-byte multiples), then the scale blocks.  (new_empty
+    with the sizes as arguments takes the host 1.5 us, torch.empty 2.3.)"""
+    if rows < 0 or K < 32 or K % 32:
+        raise ValueError("need rows >= 0 and K a positive multiple of 32")
+    m = Mx4Matrix.__new__(Mx4Matrix)
+    nc = rows * (K >> 1)
+    m._like = buf = like.new_empty(nc + ((rows + 127) >> 7) * ((K + 127) >> 7) * 512, dtype=_u8)
+    ptr = buf.data_ptr()
+    m._ptrs = ptr, ptr + nc
+    m.rows, m.K, m.device = rows, K, buf.device
+    return m
+
+
 def _mx4_out(out, rows: int, K: int, like) -> Mx4Matrix:
-    """The matrix for a result: `out`, or new buffers on the device of `like`
-    (tensor.new_empty takes less of the host than torch.empty)."""
+    """The matrix for a result: `out`, or new buffers on the device of `like`."""
     if out is None:
-        return Mx4Matrix._new(rows, K, like.new_empty)
+        return _new_mx4(rows, K, like)
     if (out.rows, out.K) != (rows, K) or out.device != like.device:
         raise ValueError(f"out is {out.rows} x {out.K} on {out.device}, expected {rows} x {K} on {like.device}")
     return out
@@ -574,13 +561,20 @@ def mx4_quantize(X, out: Mx4Matrix | None = None, stream=None) -> Mx4Matrix:
     if _torch is None:
         _init()
     rows, K, ld = _rows(X, "X")
-    return _call(_quantize, X.device, stream, X, _dtype_code(X.dtype), rows, K, ld, out)
+    dt = _dtype_code(X.dtype)
+    device = X.device
+    if stream is None and device.index == _get_device():
+        return _quantize(X, dt, rows, K, ld, out, _raw_stream(device.index))
+    with _On(device, stream) as st:
+        return _quantize(X, dt, rows, K, ld, out, st)
 
 
 def _from_nested(weights, r, out, st):
     w = weights.view(r)
     out = _mx4_out(out, w.N, w.K, weights.planes)
-    _check(lib.mq_mx4_from_nested(w, *out._ptrs, st))
+    s = lib.mq_mx4_from_nested(w, *out._ptrs, st)
+    if s:
+        _check(s)
     return out
 
 
@@ -588,15 +582,20 @@ def mx4_from_nested(weights: NestedWeights, r: int, out: Mx4Matrix | None = None
     """The r-bit model of a nested parent in MXFP4."""
     if _torch is None:
         _init()
-    return _call(_from_nested, weights.planes.device, stream, weights, r, out)
+    device = weights.planes.device
+    if stream is None and device.index == _get_device():
+        return _from_nested(weights, r, out, _raw_stream(device.index))
+    with _On(device, stream) as st:
+        return _from_nested(weights, r, out, st)
 
 
-def _dequantize(m, dtype, out, st):
+def _dequantize(m, dtype, dt, out, st):
     if out is None:
-        out, ld = m._like.new_empty((m.rows, m.K), dtype=dtype), m.K
+        ld = m.K
+        out = m._like.new_empty(m.rows, ld, dtype=dtype)
     else:
         ld = _given(out, "out", m.rows, m.K, dtype, m.device)
-    s = lib.mq_mx4_dequantize(m.struct, out.data_ptr(), _dtype_code(dtype), ld, st)
+    s = lib.mq_mx4_dequantize(m.struct, out.data_ptr(), dt, ld, st)
     if s:
         _check(s)
     return out
@@ -604,11 +603,14 @@ def _dequantize(m, dtype, out, st):
 
 def mx4_dequantize(m: Mx4Matrix, dtype=None, out=None, stream=None):
     """The values m stands for, bf16 (default) or fp32; both hold them exactly."""
-    if _torch is None:
-        _init()
     if dtype is None:
         dtype = out.dtype if out is not None else _torch.bfloat16
-    return _call(_dequantize, m.device, stream, m, dtype, out)
+    dt = _dtype_code(dtype)
+    device = m.device
+    if stream is None and device.index == _get_device():
+        return _dequantize(m, dtype, dt, out, _raw_stream(device.index))
+    with _On(device, stream) as st:
+        return _dequantize(m, dtype, dt, out, st)
 
 
 def _mx4_y(Y, M: int, w: Mx4Matrix, dtype):
@@ -616,8 +618,8 @@ def _mx4_y(Y, M: int, w: Mx4Matrix, dtype):
     if Y is None:
         if dtype is None:
             dtype = _torch.bfloat16
-        dt, N = _dtype_code(dtype), w.rows
-        return w._like.new_empty((M, N), dtype=dtype), dt, N
+        N = w.rows
+        return w._like.new_empty(M, N, dtype=dtype), _dtype_code(dtype), N
     if dtype is None:
         dtype = Y.dtype
     dt = _dtype_code(dtype)
@@ -638,7 +640,10 @@ def mx4_gemm(X: Mx4Matrix, w: Mx4Matrix, Y=None, dtype=None, stream=None):
     device = w.device
     if X.device != device:
         raise ValueError("X and w are on different devices")
-    return _call(_gemm4, device, stream, X, w, Y, dtype)
+    if stream is None and device.index == _get_device():
+        return _gemm4(X, w, Y, dtype, _raw_stream(device.index))
+    with _On(device, stream) as st:
+        return _gemm4(X, w, Y, dtype, st)
 
 
 def _gemm16(X, M, ldx, w, Y, dtype, st):
@@ -655,8 +660,6 @@ def _gemm16(X, M, ldx, w, Y, dtype, st):
 
 def mx4_gemm_bf16(X, w: Mx4Matrix, Y=None, dtype=None, stream=None):
     """Y = X . w^T with X in bf16 [M, K] as it is, w in MXFP4."""
-    if _torch is None:
-        _init()
     M, K, ldx = _rows(X, "X")
     if K != w.K:
         raise ValueError(f"X has {K} columns, expected {w.K}")
@@ -665,4 +668,7 @@ def mx4_gemm_bf16(X, w: Mx4Matrix, Y=None, dtype=None, stream=None):
     device = w.device
     if X.device != device:
         raise ValueError("X and w are on different devices")
-    return _call(_gemm16, device, stream, X, M, ldx, w, Y, dtype)
+    if stream is None and device.index == _get_device():
+        return _gemm16(X, M, ldx, w, Y, dtype, _raw_stream(device.index))
+    with _On(device, stream) as st:
+        return _gemm16(X, M, ldx, w, Y, dtype, st)
