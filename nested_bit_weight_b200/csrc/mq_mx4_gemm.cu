@@ -4,7 +4,8 @@
 // and applies both operands' power-of-two scales itself, so nothing is
 // decoded: a CTA streams codes and scales to shared memory and issues MMAs.
 // With bf16 activations every row of X is eight MXFP4 rows whose sum it is
-// (mq_mx4.cuh), and the epilogue adds their eight columns of D.
+// (mq_mx4.cuh), and the epilogue adds their eight columns of D.  This kernel
+// serves up to 128 MXFP4 rows; more go to the pair product (mq_mx4_pair.cu).
 //
 // Weights are the MMA's M operand (128 rows a tile), rows of X its N operand
 // (BN of them), so that a few tokens still fill the tensor core.
@@ -28,6 +29,11 @@
 //
 // Programmatic dependent launch: nothing is read or written before
 // griddepcontrol.wait; the weights are only brought into L2 before it.
+//
+// Bound by HBM for large weights (one token through 28672 x 8192: 23 us, 5.5 TB/s),
+// by its start and end for small ones (1024 x 4096: 3.6 us, 14336 x 4096: 8.6 us
+// of which 4.8 are HBM's), above 64 rows by the parts' way to their owner
+// (128 x 4096 x 14336: 14 us).
 //
 // Every wait is bounded (about a second); one that gives up sets a CTA abort
 // flag and the device flag read by mq_device_status.  Copies and MMAs in
@@ -129,8 +135,8 @@ __device__ __forceinline__ void store4(const MxArgs &a, int m0, int64_t n, const
     }
 }
 
-// The accumulator's `live` columns (for SLICES eight of them add to one) of this
-// thread's row, four at a time, to put(column, values).
+// The accumulator's `live` columns of this thread's row (with slices, each the
+// sum of eight), four at a time, to put(column, values).
 template <int BN, class Put>
 __device__ __forceinline__ void read_columns(uint32_t base, int slices, int live, Put put) {
     constexpr int kStep = BN < 32 ? BN : 32;
@@ -198,7 +204,7 @@ __device__ __forceinline__ void epilogue(const MxArgs &a, uint32_t base, float *
     if (groups <= 0) return;
     // never cut short, also when this CTA gave up: until then stores to this
     // CTA's memory may be on their way
-    const bool got = mbar_wait_bounded(sent, 0);
+    const bool got = mbar_wait_cluster_bounded(sent, 0);
     if (!got) flags[0] = 1;
     if (!got || !ok) return;
 #pragma unroll 2
@@ -224,7 +230,8 @@ mx4_gemm_kernel(const __grid_constant__ MxArgs a) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     float *parts = reinterpret_cast<float *>(smem + kS * C::kStage);
-    uint64_t *full = reinterpret_cast<uint64_t *>(smem + kS * C::kStage + C::kParts), *empty = full + kS, *done = empty + kS, *sent = done + 1;
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + kS * C::kStage + C::kParts), *empty = full + kS;
+    uint64_t *done = empty + kS, *sent = done + 1;
     volatile int *flags = reinterpret_cast<volatile int *>(sent + 1);   // [0] abort [1] loads
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sent + 1) + 4;
 
@@ -467,8 +474,9 @@ mq_status launch(const MxProduct &p, cudaStream_t st) {
     a.slices = p.slices;
     a.out = p.out;
     const int64_t tiles = (w->rows + kTileN - 1) / kTileN;
-    // K is split while the CTAs still fit the GPU once (kPerSm an SM) and each keeps kMinStages of K (two
-    // stages each: 7.2 us for 16 x 4096 x 4096, four: 5.3, six: 6.4)
+    // K is split while the CTAs still fit the GPU once (kPerSm an SM) and each keeps
+    // kMinStages of K (16 x 4096 x 4096 with two stages each took 7.2 us, with four
+    // 5.3, with six 6.4)
     a.CS = 1;
     while (a.CS < 8 && tiles * a.CS * 2 <= (BN <= 32 ? 296 : 148) && a.KT >= a.CS * 2 * kMinStages) a.CS *= 2;
     for (a.lper = 2; (a.CS << a.lper) < BN / p.slices;) ++a.lper;
