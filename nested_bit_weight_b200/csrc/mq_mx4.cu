@@ -184,13 +184,11 @@ mx_slices_kernel(const uint8_t *__restrict__ X, int64_t K, int64_t ld_bytes, uin
         Raw<MQ_BF16, 8> raw;
         if (c < K) raw.load<false>(X + m * ld_bytes + c * 2);
         else raw.zero();
-        float u[8];
-        raw.get(0, u);
+        float x[8];
+        raw.get(0, x);
         uint32_t E = mx_slice0_byte(raw.amax());
-        const bool bad = E == 255u;
-        const float inv = bad ? 0.f : mx_inverse(E);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) u[e] = bad ? 0.f : u[e] * inv;
+        __half2 u[4] = {};
+        if (E != 255u) mx_slice_start(x, mx_inverse(E), u);
         uint8_t *dst = codes + (tile * bn + local) * (K / 2) + c / 2;
 #pragma unroll
         for (int j = 0; j < S; ++j) {

@@ -92,18 +92,24 @@ __device__ __forceinline__ uint32_t mx_codes8(const float (&u)[8]) {
     return r;
 }
 
-// Eight codes to the numbers they stand for before scaling (exact in fp16).
+// Eight codes to the numbers they stand for before scaling, two a register.
 // Each byte is moved down by itself: taking the word apart with one
 // mov.b32 {a, b, c, d} loses the upper bytes when the word was put together
 // the same way just before (nvcc 12.9).
-__device__ __forceinline__ void mx_units8(uint32_t codes, float (&u)[8]) {
-    uint32_t h[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        asm("{\n .reg .b8 a;\n cvt.u8.u32 a, %1;\n cvt.rn.f16x2.e2m1x2 %0, a;\n}" : "=r"(h[i]) : "r"(codes >> (8 * i)));
+__device__ __forceinline__ void mx_halves8(uint32_t codes, __half2 (&h)[4]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h[i]));
+        uint32_t r;
+        asm("{\n .reg .b8 a;\n cvt.u8.u32 a, %1;\n cvt.rn.f16x2.e2m1x2 %0, a;\n}" : "=r"(r) : "r"(codes >> (8 * i)));
+        h[i] = *reinterpret_cast<const __half2 *>(&r);
+    }
+}
+__device__ __forceinline__ void mx_units8(uint32_t codes, float (&u)[8]) {
+    __half2 h[4];
+    mx_halves8(codes, h);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = __half22float2(h[i]);
         u[2 * i] = f.x;
         u[2 * i + 1] = f.y;
     }
@@ -127,15 +133,30 @@ __device__ __forceinline__ uint32_t mx_next_slice(uint32_t E, int j) {
     const uint32_t d = j == 0 ? 2u : 3u;
     return E == 255u ? 255u : (E > d ? E - d : 0u);
 }
-// Codes of one slice of eight numbers u (in the slice's unit); u becomes the
-// rest in the next slice's unit, 2^-step times as large.
-__device__ __forceinline__ uint32_t mx_slice_codes(float (&u)[8], uint32_t step) {
-    const uint32_t c = mx_codes8(u);
-    float q[8];
-    mx_units8(c, q);
-    const float f = __uint_as_float((127u + step) << 23);
+// Eight numbers, already divided by slice 0's unit (at most 7), as the start of
+// the slices.  fp16 holds them: a bf16 number's 8 bits down to 2^-14 of the unit,
+// and below that what it cuts off, at most 2^-25, is less than eight slices leave.
+__device__ __forceinline__ void mx_slice_start(const float (&x)[8], float inv, __half2 (&u)[4]) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) u[i] = (u[i] - q[i]) * f;
+    for (int i = 0; i < 4; ++i) u[i] = __floats2half2_rn(x[2 * i] * inv, x[2 * i + 1] * inv);
+}
+// Codes of one slice of eight numbers u (in the slice's unit); u becomes the
+// rest in the next slice's unit, 2^-step times as large.  Both steps are exact:
+// the rest has no bit below the number's own last one and is smaller.
+__device__ __forceinline__ uint32_t mx_slice_codes(__half2 (&u)[4], uint32_t step) {
+    float f[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 t = __half22float2(u[i]);
+        f[2 * i] = t.x;
+        f[2 * i + 1] = t.y;
+    }
+    const uint32_t c = mx_codes8(f);
+    __half2 q[4];
+    mx_halves8(c, q);
+    const __half2 m = __half2half2(__ushort_as_half((unsigned short)((15u + step) << 10)));   // 2^step
+#pragma unroll
+    for (int i = 0; i < 4; ++i) u[i] = __hmul2(__hsub2(u[i], q[i]), m);
     return c;
 }
 

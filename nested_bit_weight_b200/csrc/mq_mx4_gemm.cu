@@ -357,20 +357,19 @@ mx4_gemm_kernel(const __grid_constant__ MxArgs a) {
                 const int st = i % kS;
                 const uint32_t x[4] = {next.x, next.y, next.z, next.w};
                 next = load(i + groups);
-                float u[8];
+                float f[8];
                 uint32_t a2 = 0;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    u[2 * j] = __uint_as_float(x[j] << 16);
-                    u[2 * j + 1] = __uint_as_float(x[j] & 0xFFFF0000u);
+                    f[2 * j] = __uint_as_float(x[j] << 16);
+                    f[2 * j + 1] = __uint_as_float(x[j] & 0xFFFF0000u);
                     a2 = __vmaxu2(a2, x[j] & 0x7FFF7FFFu);
                 }
                 a2 = __vmaxu2(a2, __shfl_xor_sync(0xFFFFFFFFu, a2, 1));
                 a2 = __vmaxu2(a2, __shfl_xor_sync(0xFFFFFFFFu, a2, 2));
                 uint32_t E = mx_slice0_byte(max(a2 & 0xFFFFu, a2 >> 16) << 16);
-                const float inv = E == 255u ? 0.f : mx_inverse(E);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) u[j] = E == 255u ? 0.f : u[j] * inv;
+                __half2 u[4] = {};
+                if (E != 255u) mx_slice_start(f, mx_inverse(E), u);
                 const bool ok = i < kS || mbar_wait_backoff(empty + st, (uint32_t)(i / kS - 1) & 1u, flags);
                 if (!__all_sync(0xFFFFFFFFu, ok)) break;
                 // eight rows of B: one swizzle atom; eight rows of its scales
