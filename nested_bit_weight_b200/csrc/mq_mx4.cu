@@ -186,19 +186,25 @@ mx_slices_kernel(const uint8_t *__restrict__ X, int64_t K, int64_t ld_bytes, uin
         else raw.zero();
         float x[8];
         raw.get(0, x);
-        uint32_t E = mx_slice0_byte(raw.amax());
+        const uint32_t E = mx_slice0_byte(raw.amax());
         __half2 u[4] = {};
         if (E != 255u) mx_slice_start(x, mx_inverse(E), u);
+        // scale bytes: a lane writes those of block lane % 8 for slices lane / 8, + 4
+        const uint32_t Eb = __shfl_sync(0xFFFFFFFFu, E, (lane & 7) * 4);
+        const int64_t cb = c - lane * 8 + (lane & 7) * 32;
+#pragma unroll
+        for (int h = 0; h < (S + 3) / 4; ++h) {
+            const int j = 4 * h + (lane >> 3);
+            if (j < S && cb < G * 128)
+                scales[mx_scale_at(tile * band_rows + local + j, cb >> 7, G) + ((cb >> 5) & 3)] =
+                    (uint8_t)mx_slice_byte(Eb, j);
+        }
+        if (c >= K) continue;
         uint8_t *dst = codes + (tile * bn + local) * (K / 2) + c / 2;
 #pragma unroll
-        for (int j = 0; j < S; ++j) {
-            if ((lane & 3) == 0 && c < G * 128)
-                scales[mx_scale_at(tile * band_rows + local + j, c >> 7, G) + ((lane >> 2) & 3)] = (uint8_t)E;
-            const uint32_t En = mx_next_slice(E, j);
-            const uint32_t code = mx_slice_codes(u, E - En);
-            if (c < K) *reinterpret_cast<uint32_t *>(dst + j * (K / 2)) = code;
-            E = En;
-        }
+        for (int j = 0; j < S; ++j)
+            *reinterpret_cast<uint32_t *>(dst + j * (K / 2)) =
+                mx_slice_codes(u, mx_slice_byte(E, j) - mx_slice_byte(E, j + 1));
     }
 }
 

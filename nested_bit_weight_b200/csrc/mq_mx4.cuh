@@ -128,9 +128,9 @@ __device__ __forceinline__ uint32_t mx_slice0_byte(uint32_t amax) {
     const uint32_t f = (amax >> 23) + ((amax & 0x7FFFFFu) > 0x600000u ? 1u : 0u);   // a > 1.75 * 2^k
     return (amax >> 23) == 255u ? 255u : (f > 2u ? f - 2u : 0u);
 }
-// Scale byte of slice j + 1 from that of slice j (at least 0; 255 stays).
-__device__ __forceinline__ uint32_t mx_next_slice(uint32_t E, int j) {
-    const uint32_t d = j == 0 ? 2u : 3u;
+// Scale byte of slice j from that of slice 0 (at least 0; 255 stays).
+__device__ __forceinline__ uint32_t mx_slice_byte(uint32_t E, int j) {
+    const uint32_t d = j == 0 ? 0u : 3u * (uint32_t)j - 1u;
     return E == 255u ? 255u : (E > d ? E - d : 0u);
 }
 // Eight numbers, already divided by slice 0's unit (at most 7), as the start of

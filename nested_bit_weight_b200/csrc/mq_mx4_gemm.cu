@@ -367,7 +367,7 @@ mx4_gemm_kernel(const __grid_constant__ MxArgs a) {
                 }
                 a2 = __vmaxu2(a2, __shfl_xor_sync(0xFFFFFFFFu, a2, 1));
                 a2 = __vmaxu2(a2, __shfl_xor_sync(0xFFFFFFFFu, a2, 2));
-                uint32_t E = mx_slice0_byte(max(a2 & 0xFFFFu, a2 >> 16) << 16);
+                const uint32_t E = mx_slice0_byte(max(a2 & 0xFFFFu, a2 >> 16) << 16);
                 __half2 u[4] = {};
                 if (E != 255u) mx_slice_start(f, mx_inverse(E), u);
                 const bool ok = i < kS || mbar_wait_backoff(empty + st, (uint32_t)(i / kS - 1) & 1u, flags);
@@ -378,10 +378,10 @@ mx4_gemm_kernel(const __grid_constant__ MxArgs a) {
                 sB += m * 1024 + at;
 #pragma unroll
                 for (int j = 0; j < kMxSlices; ++j) {
-                    const uint32_t En = mx_next_slice(E, j);
-                    *reinterpret_cast<uint32_t *>(sB + j * 128 + ((swz ^ (uint32_t)j) << 4)) = mx_slice_codes(u, E - En);
-                    if ((lane & 3) == 0) sf[j * 16] = (uint8_t)E;
-                    E = En;
+                    const uint32_t Ej = mx_slice_byte(E, j);
+                    *reinterpret_cast<uint32_t *>(sB + j * 128 + ((swz ^ (uint32_t)j) << 4)) =
+                        mx_slice_codes(u, Ej - mx_slice_byte(E, j + 1));
+                    if ((lane & 3) == 0) sf[j * 16] = (uint8_t)Ej;
                 }
                 fence_proxy_async_smem();                            // the tensor core reads what was written
                 __syncwarp();
