@@ -472,8 +472,8 @@ MQ_API mq_status mq_mx4_gemm(const mq_mx4 *X, const mq_mx4 *w, void *Y_dev, int 
  * 2^-12).  Blocks whose largest value is below 2^-100 lose what lies below
  * 2^-129.
  *   workspace  device buffer of mq_mx4_gemm_bf16_workspace_bytes(M, N, K)
- *              bytes (0 for M <= 2, when it may be NULL), contents arbitrary
- *              before and after.  Calls that can overlap must not share it.
+ *              bytes (may be NULL when that is 0: M <= 2, and M <= 4 up to
+ *              2^26 weights), contents arbitrary before and after.  Calls that can overlap must not share it.
  * Preconditions as mq_mx4_gemm, M <= 2^27, ldx >= K, and for more than one row
  * a row's stride a multiple of 16 bytes.
  */

@@ -20,7 +20,7 @@
 //
 // Roles: a warp that loads (TMA for the codes, bulk copies for the scales), a
 // warp that copies the scales to TMEM and issues the MMAs, four warps for the
-// epilogue.  With one or two bf16 rows (FUSED) those four make the eight MXFP4
+// epilogue.  With up to four bf16 rows (FUSED) those four make the eight MXFP4
 // rows of each row themselves, a stage at a time, straight into the MMA's
 // operand; every CTA repeats that small work, and a launch and a pass through
 // memory are saved.  Scales have their own TMEM columns for each stage of the
@@ -108,12 +108,13 @@ struct MxArgs {
     int out;                       // type of Y
 };
 
-// Up to this many bf16 rows are cut into slices inside the product.  Cutting a
-// row is one chain of dependent operations, about 800 clocks a stage, which the
-// four warps run side by side on different stages (one row) or on two stages
-// (two rows); with eight rows it took 25 us for 14336 x 4096 where a kernel of
-// its own takes 2.
-constexpr int kFusedRows = 2;
+// Whether bf16 rows are cut into slices inside the product.  Cutting a row is one
+// chain of dependent operations, about 700 clocks a stage, which the four warps run
+// side by side: on different stages (one or two rows), on different rows (three or
+// four).  That keeps up with one or two rows always; with four, 4096 x 4096 takes
+// 5.0 us against 6.5 with a kernel of its own before, 14336 x 4096 11.4 against
+// 11.3, 28672 x 8192 32.8 against 24.7, so there the weights decide.
+bool fused_rows(int64_t M, int64_t N, int64_t K) { return M <= 2 || (M <= 4 && N * K <= (int64_t)1 << 26); }
 
 template <class T>
 __device__ __forceinline__ T to(float v);
@@ -343,7 +344,7 @@ mx4_gemm_kernel(const __grid_constant__ MxArgs a) {
             // 256 columns of a row at a time, eight a lane; the next values are
             // loaded while the last are cut
             const int groups = 4 / a.M;                              // stages at a time
-            const int m = (warp - kEpiW0) % a.M, grp = (warp - kEpiW0) / a.M;
+            const int m = (warp - kEpiW0) % a.M, grp = (warp - kEpiW0) / a.M;   // grp == groups: three rows, no work
             const uint8_t *xrow = a.X + m * a.ldx_bytes + lane * 16;
             const uint32_t swz = (uint32_t)(lane >> 2), at = (uint32_t)(lane & 3) * 4;
             auto load = [&](int i) {
@@ -353,7 +354,7 @@ mx4_gemm_kernel(const __grid_constant__ MxArgs a) {
                            : make_uint4(0u, 0u, 0u, 0u);
             };
             uint4 next = load(grp);
-            for (int i = grp; i < k1 - k0; i += groups) {
+            for (int i = grp; grp < groups && i < k1 - k0; i += groups) {
                 const int st = i % kS;
                 const uint32_t x[4] = {next.x, next.y, next.z, next.w};
                 next = load(i + groups);
@@ -451,7 +452,7 @@ mq_status launch(const MxProduct &p, cudaStream_t st) {
     size_t smem;
     const cudaError_t pe = BN == 8    ? fused ? pick<8, true>(&fn, &smem) : pick<8, false>(&fn, &smem)
                            : BN == 16  ? fused ? pick<16, true>(&fn, &smem) : pick<16, false>(&fn, &smem)
-                           : BN == 32  ? pick<32, false>(&fn, &smem)
+                           : BN == 32  ? fused ? pick<32, true>(&fn, &smem) : pick<32, false>(&fn, &smem)
                            : BN == 64  ? pick<64, false>(&fn, &smem)
                                        : pick<128, false>(&fn, &smem);
     if (pe != cudaSuccess) return cuda_fail(pe, "cudaFuncSetAttribute");
@@ -596,7 +597,7 @@ extern "C" mq_status mq_mx4_gemm(const mq_mx4 *X, const mq_mx4 *w, void *Y, int 
 extern "C" size_t mq_mx4_gemm_bf16_workspace_bytes(int64_t M, int64_t N, int64_t K) {
     if (M < 1 || M > kMaxRows || N < 1 || N > kMxMaxDim || K < kMxBlock || K % kMxBlock || K > kMxMaxDim)
         return 0;
-    if (M <= kFusedRows) return 0;
+    if (fused_rows(M, N, K)) return 0;
     // the larger of the layouts (MQ_F32 takes more slices)
     const MxSlicing sl = mx_slicing(M, MQ_F32);
     return slice_code_bytes(sl, K) + (size_t)sl.bands * (size_t)mx_groups(K) * 512;
@@ -621,7 +622,7 @@ extern "C" mq_status mq_mx4_gemm_bf16(const uint16_t *X, int64_t M, int64_t ldx,
     cudaStream_t st = (cudaStream_t)stream;
     if ((s = bind_device(st)) != MQ_OK) return s;
     MxProduct p{nullptr, nullptr, M, kMxSlices, w, Y, y_dtype, ldy, nullptr, 0, {}};
-    if (M <= kFusedRows) {
+    if (fused_rows(M, w->rows, w->K)) {
         p.X = X;
         p.ldx = ldx;
         return launch(p, st);

@@ -214,7 +214,7 @@ SHAPES = [(1, 1, 32), (1, 128, 64), (1, 1024, 4096), (2, 130, 96), (3, 300, 4128
           (16, 256, 14336), (17, 1000, 288), (33, 640, 512), (64, 128, 256), (65, 200, 544), (128, 384, 1024),
           (129, 128, 4096), (255, 257, 800), (300, 1280, 2080), (1000, 700, 160), (25, 260, 288), (31, 264, 96),
           (130, 5000, 512), (200, 5001, 512), (500, 640, 1312), (385, 321, 64), (300, 1, 64), (300, 300, 32),
-          (2, 4096, 4096), (2, 5, 32), (24, 7, 32), (129, 8, 4096), (12, 20000, 160)]
+          (2, 4096, 4096), (2, 5, 32), (3, 2000, 4096), (4, 1000, 14336), (4, 17000, 4096), (24, 7, 32), (129, 8, 4096), (12, 20000, 160)]
 
 
 @pytest.mark.parametrize("out", ["bf16", "fp16", "fp32"])

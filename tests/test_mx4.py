@@ -20,8 +20,11 @@ def test_sizes():
     for rows, K in ((-1, 32), (1, 0), (1, 16), (1, 48), (1 << 31, 32), (1, 1 << 31), (0, 32)):
         assert mq.mq_mx4_code_bytes(rows, K) == 0
         assert mq.mq_mx4_scale_bytes(rows, K) == 0
-    # eight rows of codes and scales for each row of X
-    assert mq.mq_mx4_gemm_bf16_workspace_bytes(1, 4096, 4096) <= 8 * 2048 + 32 * 512
+    # rows cut inside the product need none; others eight rows of codes and scales
+    # for each row of X
+    f = mq.mq_mx4_gemm_bf16_workspace_bytes
+    assert f(1, 4096, 4096) == f(2, 28672, 8192) == f(4, 4096, 4096) == f(3, 16384, 4096) == 0
+    assert f(5, 4096, 4096) == 40 * 2048 + 32 * 512 and f(4, 28672, 8192) == 32 * 4096 + 64 * 512
     for M, N, K in ((0, 4, 32), (1, 0, 32), (1, 4, 33), (1 << 30, 4, 32)):
         assert mq.mq_mx4_gemm_bf16_workspace_bytes(M, N, K) == 0
 
