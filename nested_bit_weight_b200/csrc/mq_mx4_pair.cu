@@ -410,9 +410,11 @@ cudaError_t pick(PairFn *fn, size_t *smem) {
 constexpr int kClusters = 74;                // two CTAs each, one an SM
 
 // Clocks of a product of Ta x Tb tiles with bn rows of B: rounds of tiles, each
-// KT stages of four MMAs (bn / 2 clocks, at least 75) and about 1500 at its ends.
+// about 1500 at its ends and KT stages of four MMAs (bn / 2 clocks each, at least
+// 75) or of 19 KiB + 64 bn bytes from L2 (58 a clock).
 int64_t clocks(int64_t Ta, int64_t Tb, int bn, int64_t KT) {
-    return (Ta * Tb + kClusters - 1) / kClusters * (KT * 4 * (bn / 2 < 75 ? 75 : bn / 2) + 1500);
+    const int mma = 4 * (bn / 2 < 75 ? 75 : bn / 2), load = (19456 + 64 * bn) / 58;
+    return (Ta * Tb + kClusters - 1) / kClusters * (KT * (mma > load ? mma : load) + 1500);
 }
 
 }  // namespace
