@@ -461,8 +461,8 @@ class _On:
         if stream is None:
             stream = torch.cuda.current_stream(device)
         elif not isinstance(stream, torch.cuda.Stream):
-            ptr = getattr(stream, "cuda_stream", stream)
-            stream = torch.cuda.ExternalStream(int(ptr), device=device)
+            ptr = int(getattr(stream, "cuda_stream", stream))
+            stream = torch.cuda.ExternalStream(ptr, device=device) if ptr else torch.cuda.default_stream(device)
         if stream.device != device:
             raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
         self._ctx = torch.cuda.stream(stream)
@@ -500,6 +500,8 @@ class Mx4Matrix:
         """Uninitialised buffers for a rows x K matrix."""
         if _torch is None:
             _init()
+        if _torch.device(device).type != "cuda":
+            raise ValueError("an MXFP4 matrix lives on a GPU")
         return _new_mx4(rows, K, _torch.empty(0, device=device))
 
     @property

@@ -327,6 +327,13 @@ def test_binding_refusals_on_device():
         mq.mx4_gemm(mq.mx4_quantize(x), w4, dtype=torch.float64)
     with pytest.raises(ValueError, match="differs in dtype"):
         mq.mx4_gemm(mq.mx4_quantize(x), w4, Y=torch.empty(4, 8, device="cuda"), dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="multiple of 32"):
+        mq.Mx4Matrix.empty(4, 40, "cuda")
+    # the default stream by its handle, and an event's stream as an object
+    want = mq.mx4_gemm_bf16(x, w4)
+    torch.cuda.synchronize()
+    assert torch.equal(mq.mx4_gemm_bf16(x, w4, stream=0), want)
+    assert torch.equal(mq.mx4_gemm_bf16(x, w4, stream=torch.cuda.default_stream()), want)
 
 
 def test_no_rows():
@@ -377,6 +384,37 @@ def test_two_streams_at_once_and_explicit_streams(M):
     mq.mq_device_status()
     for i, a, b in got:
         assert torch.equal(a, want[i][0]) and torch.equal(b, want[i][1])
+
+
+def test_two_host_threads_at_once():
+    import threading
+    import torch
+    mq = _mq()
+    w4 = mq.mx4_quantize(_acts(1500, 2048, 1))
+    xs = [_acts(M, 2048, M) for M in (3, 150)]
+    want = [(mq.mx4_gemm(mq.mx4_quantize(x), w4), mq.mx4_gemm_bf16(x, w4)) for x in xs]
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(i):
+        try:
+            st = torch.cuda.Stream()
+            with torch.cuda.stream(st):
+                for _ in range(40):
+                    y = mq.mx4_gemm(mq.mx4_quantize(xs[i]), w4), mq.mx4_gemm_bf16(xs[i], w4)
+            st.synchronize()
+            if not all(torch.equal(a, b) for a, b in zip(y, want[i])):
+                bad.append(i)
+        except Exception as e:                                     # reported by the main thread
+            bad.append(e)
+
+    threads = [threading.Thread(target=work, args=(i % 2,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    mq.mq_device_status()
+    assert not bad, bad
 
 
 @pytest.mark.parametrize("M", [1, 20, 200])
