@@ -10,6 +10,7 @@ CPU or PyTorch fallback for any step.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 __all__ = [
@@ -648,10 +649,15 @@ def mx4_gemm(X: Mx4Matrix, w: Mx4Matrix, Y=None, dtype=None, stream=None):
         return _gemm4(X, w, Y, dtype, st)
 
 
+@functools.lru_cache(maxsize=1024)
+def _ws16(M: int, N: int, K: int) -> int:
+    return lib.mq_mx4_gemm_bf16_workspace_bytes(M, N, K)
+
+
 def _gemm16(X, M, ldx, w, Y, dtype, st):
     Y, dt, ldy = _mx4_y(Y, M, w, dtype)
-    # one or two rows need no workspace; it is this call's own, on its stream
-    need = mq_mx4_gemm_bf16_workspace_bytes(M, w.rows, w.K) if M > 2 else 0
+    # the workspace is this call's own, on its stream
+    need = _ws16(M, w.rows, w.K) if M > 2 else 0
     ws = w._like.new_empty(need, dtype=_u8) if need else None
     s = lib.mq_mx4_gemm_bf16(X.data_ptr(), M, ldx, w.struct, Y.data_ptr(), dt, ldy,
                              ws.data_ptr() if need else None, need, st)
