@@ -439,7 +439,9 @@ MQ_API mq_status mq_mx4_quantize(const void *X_dev, int dtype, int64_t rows, int
  * s (2^(8-r) q_r + 2^(7-r) - z), z = 128 without zero points, taken exactly (no
  * intermediate rounding) and rounded once to the format above.  Reads the
  * first r planes, so a nested checkpoint serves the 4-bit products without a
- * dense copy.  Preconditions on w as mq_gemm; the outputs as mq_mx4_quantize.
+ * dense copy.  A scale's sign (-0.0, or a negative scale of a caller's own view)
+ * goes to the elements.  Preconditions on w as mq_gemm; the outputs as
+ * mq_mx4_quantize.
  */
 MQ_API mq_status mq_mx4_from_nested(const mq_weights *w, uint8_t *codes_out, uint8_t *scales_out,
                                     void *stream);

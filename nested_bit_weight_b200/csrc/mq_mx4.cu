@@ -347,7 +347,9 @@ __device__ __forceinline__ uint32_t nested_block(const uint32_t (&P)[8], float s
             unpair(t, v[b][e], v[b][e + 1]);
             m = fmaxf(m, fmaxf(fabsf(v[b][e]), fabsf(v[b][e + 1])));
         }
-    const float a = s * m;
+    // s may carry a sign (-0.0, or a negative scale of a caller's own view): it
+    // belongs to the elements alone
+    const float a = fabsf(s) * m;
     const uint32_t E = mx_scale_byte(__float_as_uint(a));
     const float f = a > 0.f ? s * mx_inverse(E) : s;                 // all zeros: keep their signs
 #pragma unroll
