@@ -465,14 +465,12 @@ MQ_API mq_status mq_mx4_gemm(const mq_mx4 *X, const mq_mx4 *w, void *Y_dev, int 
                              void *stream);
 
 /*
- * Y = X . W^T with bf16 activations kept (weights only in 4 bits): single
+ * Y = X . W^T with bf16 activations (weights only in 4 bits): single
  * tokens and small batches.  X is M x w->K bf16, row i at element i * ldx.  A
  * row of X is written as a sum of MXFP4 rows ("slices"), which meet the weights
- * on the 4-bit tensor cores: eight slices, which leave less than 2^-22 of the
- * largest value of each block of 32; six for more than 16 rows with a 16-bit
- * y_dtype, which leave less than 2^-16 (half a step of bf16 is 2^-9, of fp16
- * 2^-12).  Blocks whose largest value is below 2^-100 lose what lies below
- * 2^-129.
+ * on the 4-bit tensor cores: always eight slices, which leave less than 2^-22 of
+ * the largest value of each block of 32.  Blocks whose largest value is below
+ * 2^-100 lose what lies below 2^-129.
  *   workspace  device buffer of mq_mx4_gemm_bf16_workspace_bytes(M, N, K)
  *              bytes (may be NULL when that is 0: M <= 2, and M <= 4 up to
  *              2^26 weights), contents arbitrary before and after.  Calls that can overlap must not share it.

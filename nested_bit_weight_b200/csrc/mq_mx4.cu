@@ -162,16 +162,16 @@ mx_quantize_kernel(const uint8_t *__restrict__ X, int64_t rows, int64_t K, int64
     }
 }
 
-// Row m of bf16 X to S rows of an MXFP4 matrix whose sum it is (mq_mx4.cuh), in
-// tiles of `tpt` rows of X: codes in row tile * bn + (m % tpt) * S + j, scales in
-// row band_rows * tile + (m % tpt) * S + j.  Rows and columns between are not
+// Row m of bf16 X to S = kMxSlices rows of an MXFP4 matrix whose sum it is
+// (mq_mx4.cuh), in tiles of `tpt` rows of X: codes in row tile * bn + (m % tpt) * S + j,
+// scales in row band_rows * tile + (m % tpt) * S + j.  Rows and columns between are not
 // written: their products fall into columns that nothing reads.  One warp: 256
-// columns of one row.  100 x 14336 in about 4 us, one chain of six dependent
+// columns of one row.  100 x 14336 in about 4 us, one chain of eight dependent
 // roundings per warp.
-template <int S>
 __global__ void __launch_bounds__(256)
 mx_slices_kernel(const uint8_t *__restrict__ X, int64_t K, int64_t ld_bytes, uint32_t C, uint32_t total,
                  uint32_t tpt, int bn, int band_rows, uint8_t *__restrict__ codes, uint8_t *__restrict__ scales) {
+    constexpr int S = kMxSlices;
     sm100::pdl_wait();                        // X may come from the previous kernel
     sm100::pdl_launch_dependents();
     const int lane = threadIdx.x & 31;
@@ -193,9 +193,9 @@ mx_slices_kernel(const uint8_t *__restrict__ X, int64_t K, int64_t ld_bytes, uin
         const uint32_t Eb = __shfl_sync(0xFFFFFFFFu, E, (lane & 7) * 4);
         const int64_t cb = c - lane * 8 + (lane & 7) * 32;
 #pragma unroll
-        for (int h = 0; h < (S + 3) / 4; ++h) {
+        for (int h = 0; h < S / 4; ++h) {
             const int j = 4 * h + (lane >> 3);
-            if (j < S && cb < G * 128)
+            if (cb < G * 128)
                 scales[mx_scale_at(tile * band_rows + local + j, cb >> 7, G) + ((cb >> 5) & 3)] =
                     (uint8_t)mx_slice_byte(Eb, j);
         }
@@ -451,9 +451,8 @@ mq_status launch_mx_slices(const uint16_t *X, int64_t M, int64_t K, int64_t ldx,
     Steps n;
     if (!steps_for(M, K, 256, &n)) return fail(MQ_ERR_UNSUPPORTED, "mq_mx4_gemm_bf16: X is too large");
     const cudaError_t e =
-        launch_pdl(sl.S == 6 ? mx_slices_kernel<6> : mx_slices_kernel<8>, n.grid, 256, st,
-                   reinterpret_cast<const uint8_t *>(X), K, ldx * 2, n.C, n.total, sl.tpt, sl.bn, sl.Tb ? 256 : 128,
-                   codes, scales);
+        launch_pdl(mx_slices_kernel, n.grid, 256, st, reinterpret_cast<const uint8_t *>(X), K, ldx * 2, n.C, n.total,
+                   sl.tpt, sl.bn, sl.Tb ? 256 : 128, codes, scales);
     return e == cudaSuccess ? MQ_OK : cuda_fail(e, "mx_slices_kernel");
 }
 

@@ -25,14 +25,16 @@ bool mx_encode_scales(CUtensorMap *map, const uint8_t *scales, int64_t rows, int
 // rows, 128-byte swizzle; the row stride must be a multiple of 16 bytes.
 bool mx_encode_y(CUtensorMap *map, void *Y, int64_t M, int64_t N, int64_t ldy, int out);
 
-// How M bf16 rows lie as MXFP4 rows (a workspace of the product): S slices a row,
+// How M bf16 rows lie as MXFP4 rows (a workspace of the product): kMxSlices a row,
 // `tpt` rows of X a tile of `bn` MXFP4 rows; a tile's scales start a row band of
 // their own.  Tb = 0: one tile, of the kernel for few rows.
 struct MxSlicing {
-    int S, Tb, tpt, bn;
+    int Tb, tpt, bn;
     int64_t rows, bands;           // MXFP4 rows, row bands of scales
 };
-MxSlicing mx_slicing(int64_t M, int out);
+MxSlicing mx_slicing(int64_t M, int64_t N);   // N: output features
+mq_status launch_mx_slices(const uint16_t *X, int64_t M, int64_t K, int64_t ldx, const MxSlicing &sl,
+                           uint8_t *codes, uint8_t *scales, cudaStream_t st);
 
 // One product: X of M MXFP4 rows (slices = 1) or as laid out by `slice`, w of N rows.
 struct MxProduct {
@@ -120,9 +122,13 @@ __device__ __forceinline__ void mx_units8(uint32_t codes, float (&u)[8]) {
 // grid leaves at most 1 unit (up to 5 by half a step, above 5 to 6).  In units
 // a quarter as large that rest is at most 4, where the grid's half step is
 // 1/2; in units an eighth as large again at most 4, and so on.  After S slices
-// the rest is at most 2^(e0 - 3 (S - 1)): below 2^-22 a with eight, 2^-16 a with
-// six (a > 3.5 * 2^e0).
-constexpr int kMxSlices = 8;                 // slices unless mx_slicing takes fewer
+// the rest is at most 2^(e0 - 3 (S - 1)): below 2^-22 a with eight (a > 3.5 * 2^e0).
+// Always eight, whatever the output's type: how much of an element must stay is
+// not for the output's last bit to say, since a block's largest element may meet
+// weights of zero and leave the output to elements a thousandth its size.  Six
+// slices, 2^-16 a, kept only six bits of those (256 x 14336 x 4096: 35 us with
+// six, 43 with eight).
+constexpr int kMxSlices = 8;
 
 __device__ __forceinline__ uint32_t mx_slice0_byte(uint32_t amax) {
     const uint32_t f = (amax >> 23) + ((amax & 0x7FFFFFu) > 0x600000u ? 1u : 0u);   // a > 1.75 * 2^k

@@ -47,8 +47,6 @@
 #include "mq_sm100.cuh"
 
 namespace mq {
-mq_status launch_mx_slices(const uint16_t *X, int64_t M, int64_t K, int64_t ldx, const MxSlicing &sl,
-                           uint8_t *codes, uint8_t *scales, cudaStream_t st);
 namespace {
 
 using namespace sm100;
@@ -598,8 +596,7 @@ extern "C" size_t mq_mx4_gemm_bf16_workspace_bytes(int64_t M, int64_t N, int64_t
     if (M < 1 || M > kMaxRows || N < 1 || N > kMxMaxDim || K < kMxBlock || K % kMxBlock || K > kMxMaxDim)
         return 0;
     if (fused_rows(M, N, K)) return 0;
-    // the larger of the layouts (MQ_F32 takes more slices)
-    const MxSlicing sl = mx_slicing(M, MQ_F32);
+    const MxSlicing sl = mx_slicing(M, N);
     return slice_code_bytes(sl, K) + (size_t)sl.bands * (size_t)mx_groups(K) * 512;
 }
 
@@ -627,7 +624,7 @@ extern "C" mq_status mq_mx4_gemm_bf16(const uint16_t *X, int64_t M, int64_t ldx,
         p.ldx = ldx;
         return launch(p, st);
     }
-    p.slice = mx_slicing(M, y_dtype);
+    p.slice = mx_slicing(M, w->rows);
     uint8_t *codes = static_cast<uint8_t *>(workspace), *scales = codes + slice_code_bytes(p.slice, w->K);
     if ((s = launch_mx_slices(X, M, w->K, ldx, p.slice, codes, scales, st)) != MQ_OK) return s;
     p.xcodes = codes;

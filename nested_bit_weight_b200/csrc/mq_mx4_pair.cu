@@ -13,8 +13,8 @@
 //                 features; 32-row pieces go through shared memory to TMA stores.
 //   columns form  (S >= 1) A = w, B = X: a lane holds a feature, so that a warp
 //                 stores 32 neighbours of a row of Y whatever Y's alignment.  S = 1
-//                 where Y does not allow TMA stores, S = 6 or 8 for bf16
-//                 activations: S columns of D add to one output.
+//                 where Y does not allow TMA stores, S = 8 for bf16 activations:
+//                 eight columns of D add to one output.
 //
 // Persistent clusters, tiles dealt in turn (rows of A fastest, so that the
 // clusters at work share B tiles in L2).  Tensor memory: two accumulators and
@@ -346,13 +346,8 @@ mx4_pair_kernel(const __grid_constant__ PairArgs a) {
                 for (int c = 0; c * S < a.bn && m0 + c < mend; c += kRows) {
                     uint32_t v[kCols];
                     float y[kRows];
-                    if constexpr (kCols % 32 == 0) {
 #pragma unroll
-                        for (int e = 0; e < kCols / 32; ++e) tmem_ld32(d + c * S + 32 * e, v + 32 * e);
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < kCols / 16; ++e) tmem_ld16(d + c * S + 16 * e, v + 16 * e);
-                    }
+                    for (int e = 0; e < kCols / 32; ++e) tmem_ld32(d + c * S + 32 * e, v + 32 * e);
                     tmem_ld_wait();
 #pragma unroll
                     for (int e = 0; e < kRows; ++e) {
@@ -421,24 +416,25 @@ int64_t clocks(int64_t Ta, int64_t Tb, int bn, int64_t KT) {
 
 bool mx_pair_takes(const MxProduct &p) { return p.slices != 1 ? p.slice.Tb > 0 : p.M > 128; }
 
-MxSlicing mx_slicing(int64_t M, int out) {
+MxSlicing mx_slicing(int64_t M, int64_t N) {
     MxSlicing s{};
     if (M * kMxSlices <= 128) {                  // one tile of the kernel for few rows
-        s.S = kMxSlices;
         s.tpt = (int)M;
         s.rows = M * kMxSlices;
         s.bands = 1;
         s.bn = (int)s.rows;
         return s;
     }
-    // Six slices leave at most 2^-16 of a block's largest value, far below half
-    // a step of a 16-bit output (2^-9, 2^-12), and take a quarter less of the
-    // tensor cores' time, which bounds this product; fp32 outputs keep eight.
-    s.S = out == MQ_F32 ? 8 : 6;
-    const int most = 192 / s.S;
+    // 24 rows of X a tile; 32 where only that lets the clusters take all tiles at
+    // once (100 x 4096 x 14336: 24.4 us, with 24 rows and a second round for six of
+    // 80 tiles 32.3).  Elsewhere the narrower tile is ahead, with its two whole
+    // accumulators and fewer columns that wait for L2 (128 x 14336 x 4096: 26.5
+    // against 29.2, 32 x 4096 x 4096: 9.1 against 10.4).
+    const int64_t Ta = (N + 255) / 256;
+    const int most = Ta * ((M + 23) / 24) > kClusters && Ta * ((M + 31) / 32) <= kClusters ? 32 : 24;
     s.Tb = (int)((M + most - 1) / most);
     s.tpt = (int)((M + s.Tb - 1) / s.Tb);        // rows of X dealt evenly
-    s.bn = (s.tpt * s.S + 15) / 16 * 16;
+    s.bn = (s.tpt * kMxSlices + 15) / 16 * 16;
     s.rows = (int64_t)s.Tb * s.bn;
     s.bands = (int64_t)s.Tb * 2;
     return s;
@@ -488,7 +484,7 @@ mq_status launch_mx_pair(const MxProduct &p, cudaStream_t st) {
             Tb = p.slice.Tb;
             xrows = p.slice.rows;
             sfrows = p.slice.bands * 128;
-            e = p.slice.S == 6 ? pick<192, 6>(&fn, &smem) : pick<192, 8>(&fn, &smem);
+            e = a.bn > 192 ? pick<256, kMxSlices>(&fn, &smem) : pick<192, kMxSlices>(&fn, &smem);
         }
         maps = mx_encode_codes(&a.amap, w->codes, w->rows, w->K, 128) &&
                mx_encode_scales(&a.asmap, w->scales, w->rows, w->K, 1) &&

@@ -68,3 +68,27 @@ def product_bound(X: np.ndarray, W: np.ndarray, adds: int, out_eps: float, tiny:
     mag = np.abs(X) @ np.abs(W).T
     err = adds * 2.0 ** -23 * mag
     return Y, err + out_eps * (np.abs(Y) + err) + tiny
+
+
+def slices(x: np.ndarray, count: int) -> list:
+    """x [rows, K] (bf16 numbers) as the values of `count` MXFP4 matrices, a
+    greedy sum: the first has the least unit 2^e0 with a <= 7 2^e0 in each
+    block, the second a quarter of it, each later one an eighth of the one
+    before (units of at least 2^-127); each is the nearest grid point to what
+    the ones before leave."""
+    rows, K = x.shape
+    rest = np.asarray(x, np.float64).reshape(rows, K // BLOCK, BLOCK).copy()
+    a = np.abs(rest).max(axis=2)
+    m, ex = np.frexp(a)                                  # a = m 2^ex, 0.5 <= m < 1
+    e = np.where(a > 0, ex - 3 + (m > 0.875), -127)      # 7 2^e0 = 0.875 2^(e0 + 3)
+    out = []
+    for j in range(count):
+        unit = np.ldexp(1.0, np.maximum(e - (3 * j - 1 if j else 0), -127))[:, :, None]
+        u = np.abs(rest) / unit
+        hi = np.clip(np.searchsorted(GRID, u, side="left"), 1, 7)
+        dl, dh = u - GRID[hi - 1], GRID[hi] - u
+        idx = np.where(dl < dh, hi - 1, np.where(dl > dh, hi, np.where(hi % 2 == 0, hi, hi - 1)))
+        q = np.copysign(GRID[idx], rest) * unit
+        rest -= q
+        out.append(q.reshape(rows, K))
+    return out
