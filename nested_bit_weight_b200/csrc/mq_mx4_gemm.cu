@@ -37,7 +37,8 @@
 //
 // Every wait is bounded (about a second); one that gives up sets a CTA abort
 // flag and the device flag read by mq_device_status.  Copies and MMAs in
-// flight land before the CTA exits.
+// flight land before the CTA exits, and a CTA that gave up stays until the others
+// of its cluster have ended or given up too, since they may still send it parts.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -61,8 +62,10 @@ __device__ unsigned int g_mx_timeout;        // set when a bounded wait gave up
 
 #ifdef MQ_TEST_HOOKS
 // Test-hook builds only: while positive, a CTA drops its loads, so that the
-// waits for them run out (the timeout path, with no fault and no trap).
-__device__ int g_test_drop_mx4;
+// waits for them run out (the timeout path, with no fault and no trap); while
+// set, the last CTA of each cluster sends its parts only after the others' waits
+// for them have run out.
+__device__ int g_test_drop_mx4, g_test_late_mx4;
 #endif
 
 template <int BN>
@@ -192,6 +195,10 @@ __device__ __forceinline__ void epilogue(const MxArgs &a, uint32_t base, float *
     const int lper = a.lper, first = rank << lper, left = a.M - first, per = 1 << lper;
     const int groups = ((left < per ? left : per) + 3) / 4;   // of four columns owned; <= 0: none
     float4 *const p4 = reinterpret_cast<float4 *>(parts);     // [CTA][group][row]
+#ifdef MQ_TEST_HOOKS
+    if (g_test_late_mx4 && rank == a.CS - 1)
+        for (const uint64_t t0 = global_ns(); global_ns() - t0 < 4 * kWaitNs;) __nanosleep(1000);
+#endif
     if (ok) {
         const uint32_t to0 = smem_u32(p4 + ((size_t)rank << (lper - 2)) * kTileN + row), bar0 = smem_u32(sent);
         read_columns<BN>(base, a.slices, a.M, [&](int col, const float (&y)[4]) {
@@ -201,8 +208,8 @@ __device__ __forceinline__ void epilogue(const MxArgs &a, uint32_t base, float *
     }
     tmem_read();
     if (groups <= 0) return;
-    // never cut short, also when this CTA gave up: until then stores to this
-    // CTA's memory may be on their way
+    // also when this CTA gave up: until then stores to this CTA's memory may be on
+    // their way (after a wait that runs out, see the end of the kernel)
     const bool got = mbar_wait_cluster_bounded(sent, 0);
     if (!got) flags[0] = 1;
     if (!got || !ok) return;
@@ -415,10 +422,22 @@ mx4_gemm_kernel(const __grid_constant__ MxArgs a) {
 
     // ---- end: copies in flight land (already so unless a wait gave up)
     __syncthreads();
-    if (threadIdx.x == 0 && flags[0]) {
+    const bool gave_up = flags[0] != 0;                       // set by nobody from here on
+    if (threadIdx.x == 0 && gave_up) {
         atomicOr(&g_mx_timeout, 1u);
         for (int s = 0; s < kS && s < flags[1]; ++s)
             mbar_wait_bounded(full + s, (uint32_t)((flags[1] - 1 - s) / kS) & 1u);
+    }
+    __syncwarp();
+    if (a.CS > 1 && gave_up) {
+        // A CTA of the cluster that is only late still sends its parts here.  Every
+        // CTA ends (its waits are bounded) or comes to this barrier, and a thread
+        // that has ended counts as arrived, so CTAs whose waits held pay nothing;
+        // then a millisecond for stores issued just before (they take microseconds)
+        cluster_arrive();
+        cluster_wait();
+        if (threadIdx.x == 0)
+            for (const uint64_t t0 = global_ns(); global_ns() - t0 < 1000000ull;) __nanosleep(1000);
     }
     __syncthreads();                                          // shared memory stays until then
 }
@@ -640,5 +659,9 @@ int pair_test_drop(int n);
 extern "C" __attribute__((visibility("default"))) int mq_test_drop_mx4_loads(int n) {
     const int e = mq::pair_test_drop(n);
     return e ? e : (int)cudaMemcpyToSymbol(mq::g_test_drop_mx4, &n, sizeof(n));
+}
+// Make the last CTA of each cluster send its parts late (0: no longer).
+extern "C" __attribute__((visibility("default"))) int mq_test_late_mx4_parts(int on) {
+    return (int)cudaMemcpyToSymbol(mq::g_test_late_mx4, &on, sizeof(on));
 }
 #endif
