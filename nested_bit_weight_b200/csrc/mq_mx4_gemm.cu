@@ -145,6 +145,7 @@ __device__ __forceinline__ void read_columns(uint32_t base, int slices, int live
 #pragma unroll 1
     for (int c = 0; c < BN; c += kStep) {
         if (c / slices >= live) break;
+        __syncwarp();                        // lanes of features beyond N left the last stores early
         uint32_t v[kStep];
         if constexpr (kStep == 8) tmem_ld8(base + c, v);
         else if constexpr (kStep == 16) tmem_ld16(base + c, v);
@@ -175,6 +176,7 @@ __device__ __forceinline__ void read_columns(uint32_t base, int slices, int live
 // while it waited for one that still wants them could lock up with another
 // kernel's cluster that does the same the other way round.
 __device__ __forceinline__ void tmem_read() {
+    __syncwarp();
     tc_fence_before();
     named_arrive(2, 160);
 }

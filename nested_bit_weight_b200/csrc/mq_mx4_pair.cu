@@ -301,6 +301,7 @@ mx4_pair_kernel(const __grid_constant__ PairArgs a) {
 #pragma unroll 1
                 for (int p = 0; p < kChunks; ++p) {
                     const int c0 = kCols * ((p + first) % kChunks);
+                    __syncwarp();                                    // one lane issued the last piece
                     uint32_t v[kCols];
 #pragma unroll
                     for (int e = 0; e < kCols / 32; ++e) tmem_ld32(d + c0 + 32 * e, v + 32 * e);
@@ -344,6 +345,7 @@ mx4_pair_kernel(const __grid_constant__ PairArgs a) {
                 const int rows = S == 1 ? a.bn : a.tpt, m0 = tb * rows, mend = a.M - m0 < rows ? a.M : m0 + rows;
 #pragma unroll 1
                 for (int c = 0; c * S < a.bn && m0 + c < mend; c += kRows) {
+                    __syncwarp();                                    // lanes beyond N left the last stores early
                     uint32_t v[kCols];
                     float y[kRows];
 #pragma unroll
@@ -375,6 +377,7 @@ mx4_pair_kernel(const __grid_constant__ PairArgs a) {
         const uint64_t t0 = global_ns();
         while (global_ns() - t0 < 1000000ull) __nanosleep(1000);
     }
+    __syncwarp();
     tc_fence_before();
     __syncthreads();
     cluster_arrive();                                                // the peer reads this CTA's memory until here
