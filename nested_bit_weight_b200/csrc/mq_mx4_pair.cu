@@ -443,9 +443,41 @@ MxSlicing mx_slicing(int64_t M, int64_t N) {
     return s;
 }
 
+namespace {
+
+// Form and tiles of a product.
+struct PairPlan {
+    int S, bn;                     // as the kernel's template argument and PairArgs::bn
+    int64_t Ta, Tb;
+};
+PairPlan pair_plan(const MxProduct &p) {
+    const int64_t N = p.w->rows, KT = (p.w->K + kTileK - 1) / kTileK;
+    const int size = p.out == MQ_F32 ? 4 : 2;
+    if (p.slices != 1) return {kMxSlices, p.slice.bn, (N + 255) / 256, p.slice.Tb};
+    // the cheapest of the widths, the widest first
+    auto cheapest = [KT](int64_t Ta, int64_t B, int bn, int bn1, int bn2) {
+        for (int b : {bn1, bn2})
+            if (clocks(Ta, (B + b - 1) / b, b, KT) < clocks(Ta, (B + bn - 1) / bn, bn, KT)) bn = b;
+        return bn;
+    };
+    // TMA stores want row strides in 16 bytes (below 2^40), and cut a box off at
+    // the tensor's edge in steps of 16 bytes only
+    if (p.ldy * size % 16 == 0 && N * size % 16 == 0 && p.ldy < ((int64_t)1 << 36)) {
+        const int64_t Ta = (p.M + 255) / 256;
+        const int bn = cheapest(Ta, N, 256, 192, 128);
+        return {0, bn, Ta, (N + bn - 1) / bn};
+    }
+    const int64_t Ta = (N + 255) / 256;
+    const int bn = cheapest(Ta, p.M, 192, 128, 64);
+    return {1, bn, Ta, (p.M + bn - 1) / bn};
+}
+
+}  // namespace
+
 mq_status launch_mx_pair(const MxProduct &p, cudaStream_t st) {
     const mq_mx4 *w = p.w;
-    const int size = p.out == MQ_F32 ? 4 : 2;
+    const PairPlan plan = pair_plan(p);
+    const int64_t Ta = plan.Ta, Tb = plan.Tb;
     PairArgs a{};
     a.Y = p.Y;
     a.ldy = p.ldy;
@@ -454,37 +486,23 @@ mq_status launch_mx_pair(const MxProduct &p, cudaStream_t st) {
     a.K = w->K;
     a.KT = (int)((w->K + kTileK - 1) / kTileK);
     a.out = p.out;
+    a.bn = plan.bn;
     PairFn fn;
     size_t smem;
     cudaError_t e;
-    int64_t Ta, Tb;
     bool maps;
-    // TMA stores want row strides in 16 bytes (below 2^40), and cut a box off at
-    // the tensor's edge in steps of 16 bytes only
-    if (p.slices == 1 && p.ldy * size % 16 == 0 && w->rows * size % 16 == 0 && p.ldy < ((int64_t)1 << 36)) {
-        Ta = (p.M + 255) / 256;
-        a.bn = 256;
-        for (int bn : {192, 128})
-            if (clocks(Ta, (w->rows + bn - 1) / bn, bn, a.KT) < clocks(Ta, (w->rows + a.bn - 1) / a.bn, a.bn, a.KT)) a.bn = bn;
-        Tb = (w->rows + a.bn - 1) / a.bn;
+    if (plan.S == 0) {
         e = a.bn == 256 ? pick<256, 0>(&fn, &smem) : a.bn == 192 ? pick<192, 0>(&fn, &smem) : pick<128, 0>(&fn, &smem);
         maps = mx_encode_codes(&a.amap, p.xcodes, p.M, w->K, 128) && mx_encode_scales(&a.asmap, p.xscales, p.M, w->K, 1) &&
                mx_encode_codes(&a.bmap, w->codes, w->rows, w->K, a.bn / 2) &&
                mx_encode_scales(&a.bsmap, w->scales, w->rows, w->K, a.bn > 128 ? 2 : 1) &&
                mx_encode_y(&a.ymap, p.Y, p.M, w->rows, p.ldy, p.out);
     } else {
-        Ta = (w->rows + 255) / 256;
         int64_t xrows = p.M, sfrows = p.M;
-        if (p.slices == 1) {
-            a.bn = 192;
-            for (int bn : {128, 64})
-                if (clocks(Ta, (p.M + bn - 1) / bn, bn, a.KT) < clocks(Ta, (p.M + a.bn - 1) / a.bn, a.bn, a.KT)) a.bn = bn;
-            Tb = (p.M + a.bn - 1) / a.bn;
+        if (plan.S == 1) {
             e = pick<192, 1>(&fn, &smem);
         } else {
-            a.bn = p.slice.bn;
             a.tpt = p.slice.tpt;
-            Tb = p.slice.Tb;
             xrows = p.slice.rows;
             sfrows = p.slice.bands * 128;
             e = a.bn > 192 ? pick<256, kMxSlices>(&fn, &smem) : pick<192, kMxSlices>(&fn, &smem);
@@ -530,3 +548,22 @@ int pair_test_drop(int n) { return (int)cudaMemcpyToSymbol(g_test_drop_pair, &n,
 #endif
 
 }  // namespace mq
+
+#ifdef MQ_TEST_HOOKS
+// Test-hook builds only: how a product is tiled (host arithmetic alone).  Returns 0
+// (rows form), 1 or 8 (columns form, plain and sliced bf16 rows) with plan =
+// {rows of B a tile, tiles along A, tiles along B}, or -1 for the kernel for few rows.
+extern "C" __attribute__((visibility("default"))) int mq_test_mx4_plan(int64_t M, int64_t N, int64_t K, int out,
+                                                                       int64_t ldy, int bf16_rows, int64_t *plan) {
+    using namespace mq;
+    const mq_mx4 w{nullptr, nullptr, N, K};
+    MxProduct p{nullptr, nullptr, M, bf16_rows ? kMxSlices : 1, &w, nullptr, out, ldy, nullptr, 0, {}};
+    if (bf16_rows) p.slice = mx_slicing(M, N);
+    if (!mx_pair_takes(p)) return -1;
+    const PairPlan t = pair_plan(p);
+    plan[0] = t.bn;
+    plan[1] = t.Ta;
+    plan[2] = t.Tb;
+    return t.S;
+}
+#endif
