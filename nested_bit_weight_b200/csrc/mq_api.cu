@@ -47,32 +47,35 @@ static int current_context_device() {
 }
 
 mq_status bind_device(cudaStream_t st) {
+    // the last stream that answered for its device, and the device: the caller
+    // may have made another one current since
     static thread_local cudaStream_t last_stream = nullptr;
-    if (st != nullptr && st == last_stream) return MQ_OK;
-    int dev = -1;
-    cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
-    if (st != nullptr) {
-        cudaError_t e = cudaStreamIsCapturing(st, &cap);
-        if (e != cudaSuccess) return cuda_fail(e, "cudaStreamIsCapturing");
-    }
-    if (cap != cudaStreamCaptureStatusNone) {
-        // a capturing stream does not answer for its device (asking ends the
-        // capture): the caller's context, which captures on its own device
-        dev = current_context_device();
-        if (dev < 0) return MQ_OK;
-    } else if (st != nullptr) {
-        cudaError_t e = cudaStreamGetDevice(st, &dev);
-        if (e != cudaSuccess) return cuda_fail(e, "cudaStreamGetDevice");
-    } else {
-        dev = current_context_device();   // legacy stream: the caller's context
-        if (dev < 0) return MQ_OK;
+    static thread_local int last_device = -1;
+    int dev = last_device;
+    if (st == nullptr || st != last_stream) {
+        cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+        if (st != nullptr) {
+            cudaError_t e = cudaStreamIsCapturing(st, &cap);
+            if (e != cudaSuccess) return cuda_fail(e, "cudaStreamIsCapturing");
+        }
+        if (st == nullptr || cap != cudaStreamCaptureStatusNone) {
+            // the legacy stream, and a capturing stream, which does not answer for
+            // its device (asking ends the capture): the caller's context, which
+            // captures on its own device
+            dev = current_context_device();
+            if (dev < 0) return MQ_OK;
+        } else {
+            cudaError_t e = cudaStreamGetDevice(st, &dev);
+            if (e != cudaSuccess) return cuda_fail(e, "cudaStreamGetDevice");
+            last_stream = st;
+            last_device = dev;
+        }
     }
     int cur = -1;
     if (cudaGetDevice(&cur) != cudaSuccess || cur != dev) {
         cudaError_t e = cudaSetDevice(dev);
         if (e != cudaSuccess) return cuda_fail(e, "cudaSetDevice");
     }
-    last_stream = st;
     return MQ_OK;
 }
 
