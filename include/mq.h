@@ -428,8 +428,9 @@ MQ_API size_t mq_mx4_scale_bytes(int64_t rows, int64_t K);
  *   codes_out, scales_out  the two buffers (all of their bytes are written)
  * Preconditions: the sizes above, ld >= K, X and (for more than one row) the
  * bytes of a row's stride multiples of 16, the outputs 16-byte aligned and not
- * overlapping X.  rows == 0 does nothing.  MQ_ERR_UNSUPPORTED from about 2^43
- * elements on (also mq_mx4_from_nested, mq_mx4_dequantize).
+ * overlapping X.  rows == 0 does nothing.  MQ_ERR_UNSUPPORTED when a quarter of
+ * the rows (MQ_F32: half), counted in whole bands of 128, times K / 512, rounded
+ * up, is 2^31 or more: never below 2^41 elements (MQ_F32: 2^40).
  */
 MQ_API mq_status mq_mx4_quantize(const void *X_dev, int dtype, int64_t rows, int64_t K, int64_t ld,
                                  uint8_t *codes_out, uint8_t *scales_out, void *stream);
@@ -441,15 +442,19 @@ MQ_API mq_status mq_mx4_quantize(const void *X_dev, int dtype, int64_t rows, int
  * first r planes, so a nested checkpoint serves the 4-bit products without a
  * dense copy.  A scale's sign (-0.0, or a negative scale of a caller's own view)
  * goes to the elements.  Preconditions on w as mq_gemm; the outputs as
- * mq_mx4_quantize.
+ * mq_mx4_quantize.  MQ_ERR_UNSUPPORTED from 2^31 blocks of 128 x 128 on.
  */
 MQ_API mq_status mq_mx4_from_nested(const mq_weights *w, uint8_t *codes_out, uint8_t *scales_out,
                                     void *stream);
 
 /*
  * The values an MXFP4 matrix stands for: out (rows x K of type dtype, MQ_BF16
- * or MQ_F32, row i at element i * ld; both types hold every value exactly).
+ * or MQ_F32, row i at element i * ld).  Both types hold every value below 2^128
+ * exactly; larger ones, which need a scale byte of 253 or 254 and which no
+ * converter here makes, become infinities.
  * Preconditions: ld >= K, out and the bytes of a row's stride multiples of 16.
+ * MQ_ERR_UNSUPPORTED when rows / 4 times K / 512, both rounded up, is 2^31 or
+ * more: never below 2^41 elements.
  */
 MQ_API mq_status mq_mx4_dequantize(const mq_mx4 *m, void *out_dev, int dtype, int64_t ld, void *stream);
 
@@ -470,12 +475,14 @@ MQ_API mq_status mq_mx4_gemm(const mq_mx4 *X, const mq_mx4 *w, void *Y_dev, int 
  * row of X is written as a sum of MXFP4 rows ("slices"), which meet the weights
  * on the 4-bit tensor cores: always eight slices, which leave less than 2^-22 of
  * the largest value of each block of 32.  Blocks whose largest value is below
- * 2^-100 lose what lies below 2^-129.
+ * 2^-100 lose what lies below 2^-129; where the magnitudes of an output's terms
+ * add up to 2^126 or more, its sum may overflow.
  *   workspace  device buffer of mq_mx4_gemm_bf16_workspace_bytes(M, N, K)
  *              bytes (may be NULL when that is 0: M <= 2, and M <= 4 up to
  *              2^26 weights), contents arbitrary before and after.  Calls that can overlap must not share it.
  * Preconditions as mq_mx4_gemm, M <= 2^27, ldx >= K, and for more than one row
- * a row's stride a multiple of 16 bytes.
+ * a row's stride a multiple of 16 bytes.  MQ_ERR_UNSUPPORTED when M times K / 256,
+ * rounded up, is 2^31 or more.
  */
 MQ_API size_t mq_mx4_gemm_bf16_workspace_bytes(int64_t M, int64_t N, int64_t K);
 MQ_API mq_status mq_mx4_gemm_bf16(const uint16_t *X_dev, int64_t M, int64_t ldx, const mq_mx4 *w,

@@ -605,7 +605,8 @@ def _dequantize(m, dtype, dt, out, st):
 
 
 def mx4_dequantize(m: Mx4Matrix, dtype=None, out=None, stream=None):
-    """The values m stands for, bf16 (default) or fp32; both hold them exactly."""
+    """The values m stands for, bf16 (default) or fp32; both hold them exactly
+    below 2^128 (no converter here makes larger ones)."""
     if dtype is None:
         dtype = out.dtype if out is not None else _torch.bfloat16
     dt = _dtype_code(dtype)

@@ -398,8 +398,8 @@ mx_from_nested_kernel(const uint32_t *__restrict__ planes, const uint16_t *__res
     }
 }
 
-// Warp-sized steps of a converter (some columns of some rows, 32-bit numbers: a
-// matrix of 2^43 elements is refused) and blocks of eight warps for them.
+// Warp-sized steps of a converter (some columns of some rows; numbered in 32 bits,
+// 2^31 or more are refused) and blocks of eight warps for them.
 struct Steps {
     uint32_t C, total;
     int grid;
