@@ -63,7 +63,12 @@ struct PairCfg {
     static constexpr uint32_t kD1 = BN == 256 ? 128 : 192;           // second accumulator
     static constexpr uint32_t kSf = 384, kSfCols = 8 + 8 * kBands;   // scales of the stages
     static_assert(kD1 + BN <= kSf && kSf + kStages * kSfCols <= 512, "TMEM columns");
-    static constexpr size_t kSmem = 1024 + (size_t)kStages * kStage + 8 * kStg + 512;
+    // A pair holds tensor memory while its second half may still wait for some, as
+    // the clusters of the nested GEMV do; CTAs of both side by side on two SMs could
+    // each hold what the other wants.  So no pair leaves the 20 KB that the smallest
+    // of those needs beside it (the converters, which need none, still fit).
+    static constexpr size_t kNeed = 1024 + (size_t)kStages * kStage + 8 * kStg + 512,
+                            kSmem = kNeed < 207 * 1024 ? 207 * 1024 : kNeed;
     static_assert(kSmem <= 227 * 1024 && kStage % 1024 == 0, "shared memory");
 };
 
@@ -565,5 +570,12 @@ extern "C" __attribute__((visibility("default"))) int mq_test_mx4_plan(int64_t M
     plan[1] = t.Ta;
     plan[2] = t.Tb;
     return t.S;
+}
+// The least shared memory of a pair's CTA.
+extern "C" __attribute__((visibility("default"))) size_t mq_test_mx4_pair_smem() {
+    using namespace mq;
+    size_t s = PairCfg<256>::kSmem;
+    for (size_t b : {PairCfg<192>::kSmem, PairCfg<128>::kSmem}) s = b < s ? b : s;
+    return s;
 }
 #endif
