@@ -112,9 +112,11 @@ struct MxArgs {
 // Whether bf16 rows are cut into slices inside the product.  Cutting a row is one
 // chain of dependent operations, about 700 clocks a stage, which the four warps run
 // side by side: on different stages (one or two rows), on different rows (three or
-// four).  That keeps up with one or two rows always; with four, 4096 x 4096 takes
-// 5.0 us against 6.5 with a kernel of its own before, 14336 x 4096 11.4 against
-// 11.3, 28672 x 8192 32.8 against 24.7, so there the weights decide.
+// four).  That keeps up with one or two rows always.  With three or four the
+// weights decide; four rows, against a kernel of their own before: 1024 x 4096 4.8
+// us against 6.1, 4096 x 4096 5.0 against 6.4, the same from 14336 x 4096 (11.5) to
+// 8192 x 8192 (12.1 against 12.0, 2^26 weights; there it saves the workspace),
+// 10240 x 8192 19.0 against 14.6, 28672 x 8192 34 against 26.5.
 bool fused_rows(int64_t M, int64_t N, int64_t K) { return M <= 2 || (M <= 4 && N * K <= (int64_t)1 << 26); }
 
 template <class T>

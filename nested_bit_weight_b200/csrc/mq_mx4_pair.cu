@@ -5,10 +5,12 @@
 // of B as well.  The 4-bit rate is so high (16384 products a clock and SM) that a
 // tile of 256 x 256 already takes 70 bytes a clock and SM from L2 at full rate,
 // and single CTAs would take twice that (470 us where a pair takes 86).
-// Measured: 4096 x 14336 x 4096 in 86 us (5.6 PFLOP/s), 8192^3 in 177 us (6.2);
-// the power cap bounds these: the SM clock falls from 1965 to about 1450 MHz,
-// and four fifths of the cycles carry MMAs.  100 bf16 rows through 4096 x 14336:
-// 17 us, bound by L2 to shared memory.
+// Measured: 4096 x 14336 x 4096 in 86 us (5.6 PFLOP/s), 8192^3 in 179 us (6.1);
+// the power cap bounds these: the SM clock falls from 1965 to 1450-1650 MHz, and
+// two thirds to three quarters of the cycles carry MMAs.  100 bf16 rows through
+// 4096 x 14336: 24 us with the slices' own kernel (5), bound by L2 to shared memory
+// (MMAs in 47 % of the cycles); 256 rows through 14336 x 4096 43 us, where MMAs take
+// 66 %.
 //   rows form     (S = 0) A = X, B = w: a lane holds a row of Y, BN consecutive
 //                 features; 32-row pieces go through shared memory to TMA stores.
 //   columns form  (S >= 1) A = w, B = X: a lane holds a feature, so that a warp
